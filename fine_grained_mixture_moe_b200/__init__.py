@@ -13,6 +13,9 @@ from .binding import (DEBUG_FORCE_EXACT, DEBUG_PROFILE, DEBUG_WAIT_LIMIT_NS, EXP
                       moe_expert_backward, moe_backward_workspace_size, make_grads,
                       moe_debug_wait_timeout_probe, moe_expert_forward, moe_get_device_error,
                       moe_layer_forward, moe_permute, moe_profile_read, moe_quantize_fp8,
-                      moe_route, moe_route_noalloc, moe_workspace_size, status_str)
+                      moe_route, moe_route_noalloc, moe_workspace_size, status_str,
+                      moe_fp8_token_blocks, moe_gemm_fp8_block, moe_quantize_fp8_block,
+                      moe_quantize_fp8_tokens, moe_quantize_fp8_weight, moe_swiglu_fp8_backward,
+                      moe_swiglu_fp8_forward, moe_wgrad_fp8_block)
 from .layer import (MoELayer, quantize_lowrank_weights, torch_dtype, upload_weights,  # noqa: F401
                     y_perm_dtype)

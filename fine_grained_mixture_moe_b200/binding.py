@@ -22,7 +22,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
                 6: "MOE_ERR_DEVICE_CHECK"}
 SCORE = {"softmax": 0, "sigmoid": 1}
 EXPERT = {"swiglu": 0, "lowrank": 1}
-DTYPE = {"f32": 0, "bf16": 1}
+DTYPE = {"f32": 0, "bf16": 1, "e4m3": 2}
 STORAGE = {"dtype": 0, "fp8": 1}
 DEBUG_FORCE_EXACT, DEBUG_WAIT_LIMIT_NS, DEBUG_PROFILE, DEBUG_STAMP = 1, 2, 3, 4
 
@@ -116,6 +116,20 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                                         c_void_p, c_void_p, c_void_p, c_void_p]),
         "moe_quantize_fp8": (c_int32, [c_void_p, c_int32, c_int64, c_int32, c_void_p, c_void_p,
                                        c_void_p]),
+        "moe_fp8_token_blocks": (c_int64, [c_int64, c_int32]),
+        "moe_quantize_fp8_block": (c_int32, [c_void_p, c_int32, c_int64, c_int32, c_void_p,
+                                             c_void_p, c_void_p, c_void_p]),
+        "moe_quantize_fp8_weight": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_int32,
+                                              c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+        "moe_quantize_fp8_tokens": (c_int32, [c_void_p, c_int32, c_void_p, c_int64, c_int32,
+                                              c_void_p, c_int32, c_void_p, c_void_p, c_void_p]),
+        "moe_gemm_fp8_block": (c_int32, [c_void_p, c_void_p, c_int64, c_void_p, c_int32, c_int32,
+                                         c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_void_p]),
+        "moe_wgrad_fp8_block": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p,
+                                          c_int32, c_int32, c_int32, c_void_p, c_void_p]),
+        "moe_swiglu_fp8_forward": (c_int32, [c_void_p, c_int32, c_int64, c_int32] + [c_void_p] * 7),
+        "moe_swiglu_fp8_backward": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int64,
+                                              c_int32] + [c_void_p] * 6),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -132,7 +146,9 @@ EXPORTED = ("moe_workspace_size", "moe_capacity", "moe_route", "moe_permute",
             "moe_layer_forward",
             "moe_status_str", "moe_get_device_error", "moe_debug_set", "moe_profile_read",
             "moe_stamp_read", "moe_debug_wait_timeout_probe", "moe_route_noalloc",
-            "moe_quantize_fp8")
+            "moe_quantize_fp8", "moe_fp8_token_blocks", "moe_quantize_fp8_block",
+            "moe_quantize_fp8_weight", "moe_quantize_fp8_tokens", "moe_gemm_fp8_block",
+            "moe_wgrad_fp8_block", "moe_swiglu_fp8_forward", "moe_swiglu_fp8_backward")
 
 
 def _ptr(t) -> Optional[int]:
@@ -318,3 +334,150 @@ def moe_route_noalloc(cfg, x, w: MoEWeights, topk_idx, topk_w, expert_count, pro
            load().moe_route_noalloc(ctypes.byref(cfg), _ptr(x), ctypes.byref(w), _ptr(topk_idx),
                                     _ptr(topk_w), _ptr(expert_count), _ptr(prob_sum),
                                     _stream(stream)))
+
+
+# ------------------------------------------------------------------ block-scaled 8-bit operators
+# These functions also check the torch tensors they are given (an integer address is passed as it
+# is): on the current CUDA device, contiguous, of the expected type and large enough.
+BLOCK = 128
+
+
+def _nblocks(n: int) -> int:
+    return -(-n // BLOCK)
+
+
+def _buffer(fn: str, name: str, t, dtypes, numel: int) -> Optional[int]:
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if t.dtype not in dtypes:
+        raise TypeError(f"{fn}: {name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.numel() < numel:
+        raise ValueError(f"{fn}: {name} has {t.numel()} elements, needs {numel}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} is not contiguous")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on the current CUDA device")
+    return t.data_ptr()
+
+
+def _fp8_types():
+    import torch
+    return ((torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.float8_e8m0fnu),
+            (torch.bfloat16, torch.float32), (torch.int32,))
+
+
+def _value_dtype(t) -> int:
+    """DTYPE code of a tensor of values or codes."""
+    import torch
+    codes = {torch.bfloat16: DTYPE["bf16"], torch.float32: DTYPE["f32"],
+             torch.uint8: DTYPE["e4m3"], torch.float8_e4m3fn: DTYPE["e4m3"]}
+    if getattr(t, "dtype", None) not in codes:
+        raise TypeError(f"expected a bf16, fp32 or E4M3 tensor, got {getattr(t, 'dtype', type(t))}")
+    return codes[t.dtype]
+
+
+def moe_fp8_token_blocks(rows: int, E: int) -> int:
+    """Blocks of 128 rows that hold any split of `rows` rows among E experts."""
+    n = int(load().moe_fp8_token_blocks(rows, E))
+    if n < 0:
+        raise MoEError("moe_fp8_token_blocks", 2)
+    return n
+
+
+def moe_quantize_fp8_block(x, rows: int, cols: int, q, scale, n_rows=None, stream=None) -> None:
+    """E4M3 codes q [rows, cols] and E8M0 scales [rows, ceil(cols / 128)] of x (bf16 or fp32)."""
+    fn = "moe_quantize_fp8_block"
+    code, e8, val, i32 = _fp8_types()
+    _check(fn, load().moe_quantize_fp8_block(
+        _buffer(fn, "x", x, val, rows * cols), _value_dtype(x), rows, cols,
+        _buffer(fn, "n_rows", n_rows, i32, 1), _buffer(fn, "q", q, code, rows * cols),
+        _buffer(fn, "scale", scale, e8, rows * _nblocks(cols)), _stream(stream)))
+
+
+def moe_quantize_fp8_weight(w, E: int, rows: int, cols: int, q, scale, q_t=None, scale_t=None,
+                            stream=None) -> None:
+    """Codes and scales of stacked weights w [E, rows, cols] in 128 x 128 blocks, and optionally of
+    the transposed weights."""
+    fn = "moe_quantize_fp8_weight"
+    code, e8, val, _ = _fp8_types()
+    n, nb = E * rows * cols, E * _nblocks(rows) * _nblocks(cols)
+    _check(fn, load().moe_quantize_fp8_weight(
+        _buffer(fn, "w", w, val, n), _value_dtype(w), E, rows, cols,
+        _buffer(fn, "q", q, code, n), _buffer(fn, "scale", scale, e8, nb),
+        _buffer(fn, "q_t", q_t, code, n), _buffer(fn, "scale_t", scale_t, e8, nb),
+        _stream(stream)))
+
+
+def moe_quantize_fp8_tokens(x, x_scale, rows: int, cols: int, offsets, E: int, q_t, scale_t,
+                            stream=None) -> None:
+    """Transposed codes q_t [cols, 128 B] and scales [B, cols] along each expert's rows, from bf16 or
+    fp32 rows (x_scale None) or from E4M3 rows with their scales; B = moe_fp8_token_blocks."""
+    fn = "moe_quantize_fp8_tokens"
+    code, e8, val, i32 = _fp8_types()
+    nb = moe_fp8_token_blocks(rows, E)
+    _check(fn, load().moe_quantize_fp8_tokens(
+        _buffer(fn, "x", x, val + code, rows * cols), _value_dtype(x),
+        _buffer(fn, "x_scale", x_scale, e8, rows * _nblocks(cols)), rows, cols,
+        _buffer(fn, "offsets", offsets, i32, E + 1), E,
+        _buffer(fn, "q_t", q_t, code, cols * BLOCK * nb),
+        _buffer(fn, "scale_t", scale_t, e8, nb * cols), _stream(stream)))
+
+
+def moe_gemm_fp8_block(a, a_scale, rows: int, offsets, E: int, n: int, k: int, w, w_scale, out,
+                       stream=None) -> None:
+    """out [rows, n] (bf16 or fp32) = a [rows, k] w[e]^T, expert e's rows by offsets."""
+    fn = "moe_gemm_fp8_block"
+    code, e8, val, i32 = _fp8_types()
+    _check(fn, load().moe_gemm_fp8_block(
+        _buffer(fn, "a", a, code, rows * k), _buffer(fn, "a_scale", a_scale, e8, rows * _nblocks(k)),
+        rows, _buffer(fn, "offsets", offsets, i32, E + 1), E, n, k,
+        _buffer(fn, "w", w, code, E * n * k),
+        _buffer(fn, "w_scale", w_scale, e8, E * _nblocks(n) * _nblocks(k)),
+        _buffer(fn, "out", out, val, rows * n), _value_dtype(out), _stream(stream)))
+
+
+def moe_wgrad_fp8_block(a_t, a_scale, b_t, b_scale, rows: int, offsets, E: int, n: int, k: int, dw,
+                        stream=None) -> None:
+    """dw [E, n, k] (fp32) = per expert a^T b, both operands as moe_quantize_fp8_tokens wrote them."""
+    import torch
+    fn = "moe_wgrad_fp8_block"
+    code, e8, _, i32 = _fp8_types()
+    nb = moe_fp8_token_blocks(rows, E)
+    _check(fn, load().moe_wgrad_fp8_block(
+        _buffer(fn, "a_t", a_t, code, n * BLOCK * nb), _buffer(fn, "a_scale", a_scale, e8, nb * n),
+        _buffer(fn, "b_t", b_t, code, k * BLOCK * nb), _buffer(fn, "b_scale", b_scale, e8, nb * k),
+        rows, _buffer(fn, "offsets", offsets, i32, E + 1), E, n, k,
+        _buffer(fn, "dw", dw, (torch.float32,), E * n * k), _stream(stream)))
+
+
+def moe_swiglu_fp8_forward(gu, rows: int, ffn: int, h=None, h_q=None, h_scale=None, gu_q=None,
+                           gu_scale=None, n_rows=None, stream=None) -> None:
+    """h = silu(gate) * up of gu [rows, 2 ffn] in bf16 (h) and / or E4M3 (h_q, h_scale), and gu's own
+    E4M3 checkpoint (gu_q, gu_scale)."""
+    import torch
+    fn = "moe_swiglu_fp8_forward"
+    code, e8, val, i32 = _fp8_types()
+    n, nb = rows * ffn, rows * _nblocks(ffn)
+    _check(fn, load().moe_swiglu_fp8_forward(
+        _buffer(fn, "gu", gu, val, 2 * n), _value_dtype(gu), rows, ffn,
+        _buffer(fn, "n_rows", n_rows, i32, 1), _buffer(fn, "h", h, (torch.bfloat16,), n),
+        _buffer(fn, "h_q", h_q, code, n), _buffer(fn, "h_scale", h_scale, e8, nb),
+        _buffer(fn, "gu_q", gu_q, code, 2 * n), _buffer(fn, "gu_scale", gu_scale, e8, 2 * nb),
+        _stream(stream)))
+
+
+def moe_swiglu_fp8_backward(gu_q, gu_scale, dh, rows: int, ffn: int, dgu=None, dgu_q=None,
+                            dgu_scale=None, h=None, n_rows=None, stream=None) -> None:
+    """[d_gate | d_up] [rows, 2 ffn] in bf16 (dgu) and / or E4M3 (dgu_q, dgu_scale), and h again in
+    bf16, from the checkpoint gu_q, gu_scale and dh [rows, ffn]."""
+    import torch
+    fn = "moe_swiglu_fp8_backward"
+    code, e8, val, i32 = _fp8_types()
+    n, nb = rows * ffn, rows * _nblocks(ffn)
+    _check(fn, load().moe_swiglu_fp8_backward(
+        _buffer(fn, "gu_q", gu_q, code, 2 * n), _buffer(fn, "gu_scale", gu_scale, e8, 2 * nb),
+        _buffer(fn, "dh", dh, val, n), _value_dtype(dh), rows, ffn,
+        _buffer(fn, "n_rows", n_rows, i32, 1), _buffer(fn, "dgu", dgu, (torch.bfloat16,), 2 * n),
+        _buffer(fn, "dgu_q", dgu_q, code, 2 * n), _buffer(fn, "dgu_scale", dgu_scale, e8, 2 * nb),
+        _buffer(fn, "h", h, (torch.bfloat16,), n), _stream(stream)))

@@ -1,0 +1,85 @@
+// Launches of the block-scaled E4M3 operators (fp8_block.cuh, gemm_fp8_block.cuh). Included by
+// moe_lib.cu inside its unnamed namespace.
+#pragma once
+
+// [rows, cols] bytes seen as {128 columns, rows, cols / 128 K blocks} (cols a multiple of 128): a
+// box {128, 128, 2} is the tiles of two K blocks, one after the other. Rows past the last, and the
+// second K block past the last, read as zeros.
+bool make_map3_u8(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {128, rows, cols / 128};
+  cuuint64_t strides[2] = {cols, 128};
+  cuuint32_t box[3] = {128, 128, 2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(ptr), dims, strides,
+                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// Row-wise kernels: 256 threads, `per` blocks of 128 values per CTA and pass, as many CTAs as are
+// resident at once (8 per SM) or fewer.
+int fp8_row_grid(long long blocks, int per) {
+  return (int)std::max<long long>(1, std::min<long long>(8LL * num_sms(), (blocks + per - 1) / per));
+}
+
+template <typename Tin>
+moe_status_t launch_quantize_block(const void *in, long long rows, int cols, const int32_t *n_rows,
+                                   uint8_t *q, uint8_t *scale, cudaStream_t st) {
+  const int nblk = ceil_div(cols, QB), per = 256 * 16 / (int)sizeof(Tin) / QB;
+  ProfScope ps(K_F8B_QUANT, st);
+  return launch_pdl(quantize_block_rows_kernel<Tin>, dim3(fp8_row_grid(rows * nblk, per)), dim3(256), 0,
+                    st, (const Tin *)in, rows, cols, nblk, n_rows, q, scale);
+}
+
+template <typename Tin>
+moe_status_t launch_quantize_weight(const void *in, int E, int rows, int cols, uint8_t *q,
+                                    uint8_t *scale, uint8_t *q_t, uint8_t *scale_t, cudaStream_t st) {
+  ProfScope ps(K_F8B_QUANT, st);
+  return launch_pdl(quantize_block_weight_kernel<Tin>, dim3(ceil_div(cols, QB), ceil_div(rows, QB), E),
+                    dim3(F8T_THREADS), 0, st, (const Tin *)in, rows, cols, q, scale, q_t, scale_t);
+}
+
+long long token_blocks(long long rows, int E) {
+  return (rows + 127 * std::min<long long>(rows, E)) / QB;
+}
+
+template <typename Tin>
+moe_status_t launch_quantize_tokens(const void *in, const uint8_t *in_scale, long long rows, int cols,
+                                    const int32_t *offsets, int E, uint8_t *q_t, uint8_t *scale_t,
+                                    cudaStream_t st) {
+  const long long nb = token_blocks(rows, E);
+  ProfScope ps(K_F8B_QUANT, st);
+  return launch_pdl(quantize_block_tokens_kernel<Tin>, dim3((unsigned)(nb * ceil_div(cols, QB))),
+                    dim3(F8T_THREADS), 0, st, (const Tin *)in, in_scale, rows, cols, offsets, E, q_t,
+                    (size_t)(nb * QB), scale_t);
+}
+
+template <bool WGRAD>
+moe_status_t launch_gemm_fp8_block(F8Gemm &p, const uint8_t *a, const uint8_t *b, cudaStream_t st) {
+  // one row of a (b) is K codes; wgrad: the token columns of every block
+  const uint64_t lda = WGRAD ? (uint64_t)p.K * QB : (uint64_t)p.K;
+  const uint64_t a_rows = WGRAD ? p.M : p.rows, b_rows = WGRAD ? (uint64_t)p.N : (uint64_t)p.E * p.N;
+  if (WGRAD) p.K = (int)(lda / QB);
+  // two K blocks per copy when a row is whole K blocks (one 32 KB box instead of two copies) and
+  // the tile lists of E experts leave room for two such stages
+  p.kpb = lda % QB == 0 && f8g_stages(p.E, 2) >= 2 ? 2 : 1;
+  p.stages = f8g_stages(p.E, p.kpb);
+  static_assert(f8g_stages(1024, 1) >= 2, "tile lists of 1024 experts leave no room");
+  const bool ok = p.kpb == 2 ? make_map3_u8(&p.ma, a, a_rows, lda) && make_map3_u8(&p.mb, b, b_rows, lda)
+                             : make_map(&p.ma, a, a_rows, lda, 128, 1) &&
+                                   make_map(&p.mb, b, b_rows, lda, 128, 1);
+  if (!ok) return MOE_ERR_CUDA;
+  const size_t smem = f8g_smem_bytes(p.E, p.kpb);
+  auto kern = gemm_fp8_block_kernel<WGRAD>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  const long long tiles = WGRAD ? (long long)p.E * ceil_div(p.M, 256) * ceil_div(p.N, 256)
+                                : (ceil_div(p.rows, 256) + std::min<long long>(p.E, p.rows)) *
+                                      ceil_div(p.N, 256);
+  const int pairs = (int)std::min<long long>(num_sms() / 2, tiles);
+  const int kind = WGRAD ? K_F8B_WGRAD : K_F8B_GEMM;
+  ProfScope ps(kind, st);
+  return launch_pdl(kern, dim3(2 * pairs), dim3(TC_THREADS), smem, st, p);
+}

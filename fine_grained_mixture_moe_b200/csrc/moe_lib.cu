@@ -16,6 +16,8 @@
 #include "common.cuh"
 #include "f32split.cuh"
 #include "fp8.cuh"
+#include "fp8_block.cuh"
+#include "gemm_fp8_block.cuh"
 #include "gemm_tc.cuh"
 #include "gemm_tc2.cuh"
 #include "permute.cuh"
@@ -199,7 +201,8 @@ int num_sms() {
 const char *kKindName[K_COUNT] = {"router", "stats", "perm_hist", "perm_scatter", "gemm_gateup",
                                   "gemm_down", "gemm_lowrank_v", "gemm_lowrank_u", "combine",
                                   "aux_loss", "backward_gemm", "quantize_fp8",
-                                  "split_f32"};
+                                  "split_f32", "quantize_fp8_block", "swiglu_fp8",
+                                  "gemm_fp8_block", "wgrad_fp8_block"};
 constexpr int PROF_SLOTS = 8192;
 struct Prof {
   bool on = false;
@@ -829,6 +832,7 @@ moe_status_t aux_impl(const moe_config_t *c, const int32_t *count, const float *
 }
 
 #include "backward_lib.cuh"
+#include "fp8_block_lib.cuh"
 
 // ------------------------------------------------------------------ argument checks
 moe_status_t check_cfg(const moe_config_t *c) {
@@ -930,6 +934,7 @@ moe_status_t moe_combine(const moe_config_t *cfg, const void *y_perm, const void
 }
 
 #include "backward_api.cuh"
+#include "fp8_block_api.cuh"
 
 moe_status_t moe_aux_loss(const moe_config_t *cfg, const int32_t *expert_count,
                           const float *prob_sum, float *loss, void *stream) {

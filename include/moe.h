@@ -52,7 +52,8 @@ typedef enum {
 
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
 typedef enum { MOE_EXPERT_SWIGLU = 0, MOE_EXPERT_LOWRANK = 1 } moe_expert_t;
-typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1 } moe_dtype_t;
+/* MOE_DTYPE_E4M3: 8-bit codes, only where an argument of the block-scaled operators says so. */
+typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_E4M3 = 2 } moe_dtype_t;
 /* Storage of the routed experts' weights. MOE_STORAGE_FP8_E4M3 is the fp8 rung of the storage
  * ladder of the low-rank experts (dormouse, "TSCT low-rank experts": the U*diag(s)*V^T
  * factorisation carries a storage ladder fp8 -> NVFP4 -> ternary): V and U as E4M3 rows with
@@ -337,6 +338,99 @@ moe_status_t moe_route_noalloc(const moe_config_t *cfg, const void *x, const moe
  * arguments return MOE_ERR_INVALID_ARG or MOE_ERR_UNSUPPORTED with nothing enqueued. */
 moe_status_t moe_quantize_fp8(const void *in, int32_t in_dtype, int64_t rows, int32_t cols,
                               uint8_t *q, float *scale, void *stream);
+
+/* ---------------------------------------------------------------- block-scaled 8-bit operators
+ * The grouped experts in 8 bits, forward and backward (quartz-micro-preview-base card,
+ * "Architecture": the routed SwiGLU experts; the pages name fp8 only as a storage rung of the
+ * low-rank experts, so the format below is this library's).
+ *
+ * Format: E4M3 codes (as moe_quantize_fp8) and one E8M0 byte b per block of 128 values, worth
+ * 2^(b - 127): the least power of two with amax / scale <= 448, not below 2^-126; 1 for an
+ * all-zero block. code = the E4M3 value nearest to v / scale (exact quotient), ties to the even
+ * code. Three layouts:
+ *   rows    1 x 128 blocks: q [rows, cols], scale [rows, ceil(cols / 128)]
+ *   weight  128 x 128 blocks: q [E, rows, cols], scale [E, ceil(rows / 128), ceil(cols / 128)]
+ *   tokens  128 x 1 blocks along the rows of one expert, stored transposed: expert e's rows
+ *           [offsets[e], offsets[e+1]) fill blocks of 128 from its own first row, blocks numbered
+ *           through the experts in order; q_t [cols, 128 * B], scale_t [B, cols], with
+ *           B = moe_fp8_token_blocks(rows, E), which holds any split of `rows` rows. Rows that
+ *           complete an expert's last block are zeros; blocks past the last are not written.
+ * A last block along a dimension may be shorter. Scale bytes 1 .. 254 are valid on input.
+ *
+ * For all of them: widths (cols, n, k; rows of a weight) are multiples of 16 up to 2^20,
+ * 1 <= E <= 1024, rows < 2^31 - 4096 (more returns MOE_ERR_UNSUPPORTED), rows = 0 writes nothing
+ * (moe_wgrad_fp8_block: zeros). offsets: [E+1] int32 on the device, non-decreasing, as
+ * moe_permute returns them; entries are clamped to [0, rows], so no value of them reads or writes
+ * out of bounds. n_rows: a device int32, the number of leading rows to process (offsets + E skips
+ * the rows behind the last kept pair, which are neither read nor written), or NULL for all.
+ * Pointers are 16-byte aligned; scale arrays need no alignment unless stated, offsets and n_rows
+ * 4 bytes. Outputs must not overlap inputs. No workspace; safe to capture, to run on several
+ * streams at once, and to call from several threads. Values must be finite in the rows that are
+ * processed (a non-finite one makes its own block unspecified, and what is summed from it).
+ * Asynchronous on `stream`; bad arguments return MOE_ERR_INVALID_ARG or MOE_ERR_UNSUPPORTED with
+ * nothing enqueued. */
+
+/* Blocks of 128 rows that hold any split of `rows` rows among E experts,
+ * (rows + 127 min(rows, E)) / 128; -1 for rows or E outside the ranges above. */
+int64_t moe_fp8_token_blocks(int64_t rows, int32_t E);
+
+/* in [rows, cols] (MOE_DTYPE_BF16 or MOE_DTYPE_F32) to the rows layout. The same codes are the
+ * 8-bit checkpoint of `in` for the backward pass (moe_quantize_fp8_tokens reads them). */
+moe_status_t moe_quantize_fp8_block(const void *in, int32_t in_dtype, int64_t rows, int32_t cols,
+                                    const int32_t *n_rows, uint8_t *q, uint8_t *scale, void *stream);
+
+/* in [E, rows, cols] to the weight layout; q_t [E, cols, rows] and scale_t [E, ceil(cols / 128),
+ * ceil(rows / 128)] (both or neither NULL) receive the transposed weights, the operand of the
+ * input gradient: square blocks, so the codes and scales are the same ones. */
+moe_status_t moe_quantize_fp8_weight(const void *in, int32_t in_dtype, int32_t E, int32_t rows,
+                                     int32_t cols, uint8_t *q, uint8_t *scale, uint8_t *q_t,
+                                     uint8_t *scale_t, void *stream);
+
+/* in [rows, cols] to the tokens layout (a weight gradient's operand). in_dtype MOE_DTYPE_BF16 or
+ * MOE_DTYPE_F32 with in_scale NULL, or MOE_DTYPE_E4M3: `in` and in_scale are the rows layout (an
+ * 8-bit checkpoint), whose values are quantised again along the tokens. */
+moe_status_t moe_quantize_fp8_tokens(const void *in, int32_t in_dtype, const uint8_t *in_scale,
+                                     int64_t rows, int32_t cols, const int32_t *offsets, int32_t E,
+                                     uint8_t *q_t, uint8_t *scale_t, void *stream);
+
+/* Grouped product: for rows r of expert e, with the values the codes stand for,
+ *   out[r, c] = sum_i a[r, i] w[e, c, i],  c < n, i < k
+ * a, a_scale: rows layout [rows, k]; w, w_scale: weight layout [E, n, k]; out [rows, n] in bf16 or
+ * fp32 (out_dtype), rounded once from fp32 sums. The input gradient is the same call on the
+ * transposed weights. offsets may be NULL with E = 1: one weight for all rows. Rows outside every
+ * expert are not written. */
+moe_status_t moe_gemm_fp8_block(const uint8_t *a, const uint8_t *a_scale, int64_t rows,
+                                const int32_t *offsets, int32_t E, int32_t n, int32_t k,
+                                const uint8_t *w, const uint8_t *w_scale, void *out,
+                                int32_t out_dtype, void *stream);
+
+/* Weight gradient: dw[e, c, i] = sum over the rows r of expert e of a[r, c] b[r, i], c < n, i < k
+ * (a the product's upstream gradient, b its input), fp32 [E, n, k]; zeros for an expert with no
+ * rows. a_t, a_scale: tokens layout of [rows, n]; b_t, b_scale: of [rows, k] (b_scale 4-byte
+ * aligned), both made with these rows, offsets and E. */
+moe_status_t moe_wgrad_fp8_block(const uint8_t *a_t, const uint8_t *a_scale, const uint8_t *b_t,
+                                 const uint8_t *b_scale, int64_t rows, const int32_t *offsets,
+                                 int32_t E, int32_t n, int32_t k, float *dw, void *stream);
+
+/* SwiGLU that keeps its input in 8 bits: gu [rows, 2 ffn] = [gate | up] (bf16 or fp32),
+ * h = silu(gate) * up in fp32; h as bf16 to `h`, and / or in the rows layout [rows, ffn] to h_q,
+ * h_scale (the down product's operand); the checkpoint, gu in the rows layout [rows, 2 ffn], to
+ * gu_q, gu_scale. Each of the three outputs may be NULL, not all. ffn a multiple of 128 (no block
+ * spans gate and up; otherwise MOE_ERR_UNSUPPORTED). */
+moe_status_t moe_swiglu_fp8_forward(const void *gu, int32_t in_dtype, int64_t rows, int32_t ffn,
+                                    const int32_t *n_rows, void *h, uint8_t *h_q, uint8_t *h_scale,
+                                    uint8_t *gu_q, uint8_t *gu_scale, void *stream);
+
+/* Its backward from the checkpoint, with s = 1 / (1 + e^-gate) and dh [rows, ffn] (bf16 or fp32):
+ *   d_up = dh * gate s,  d_gate = dh * up s (1 + gate (1 - s)),  h = gate s up
+ * dgu = [d_gate | d_up] [rows, 2 ffn] as bf16 to `dgu`, and / or in the rows layout to dgu_q,
+ * dgu_scale (the input gradient's operand); h [rows, ffn] as bf16, the down weight gradient's
+ * other operand. Each of the three may be NULL, not all. Derivatives of the values the checkpoint
+ * holds (straight through its rounding). */
+moe_status_t moe_swiglu_fp8_backward(const uint8_t *gu_q, const uint8_t *gu_scale, const void *dh,
+                                     int32_t dh_dtype, int64_t rows, int32_t ffn,
+                                     const int32_t *n_rows, void *dgu, uint8_t *dgu_q,
+                                     uint8_t *dgu_scale, void *h, void *stream);
 
 /* Human-readable name of a status. Never NULL. */
 const char *moe_status_str(moe_status_t s);
