@@ -337,44 +337,70 @@ def moe_route_noalloc(cfg, x, w: MoEWeights, topk_idx, topk_w, expert_count, pro
 
 
 # ------------------------------------------------------------------ block-scaled 8-bit operators
-# These functions also check the torch tensors they are given (an integer address is passed as it
-# is): on the current CUDA device, contiguous, of the expected type and large enough.
+# These functions also check the torch tensors they are given: on the current CUDA device,
+# contiguous, of the expected type and large enough. An integer address is passed as it is, except
+# where the tensor's type selects the call's.
 BLOCK = 128
 
 
 def _nblocks(n: int) -> int:
-    return -(-n // BLOCK)
+    return (n + BLOCK - 1) // BLOCK
 
 
-def _buffer(fn: str, name: str, t, dtypes, numel: int) -> Optional[int]:
-    if t is None or isinstance(t, int):
-        return t
-    import torch
-    if t.dtype not in dtypes:
-        raise TypeError(f"{fn}: {name} has dtype {t.dtype}, expected one of {dtypes}")
-    if t.numel() < numel:
-        raise ValueError(f"{fn}: {name} has {t.numel()} elements, needs {numel}")
-    if not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} is not contiguous")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{fn}: {name} is on {t.device}, not on the current CUDA device")
-    return t.data_ptr()
+class _Fp8Types:
+    """Accepted types by role, and DTYPE codes; built once, on the first call."""
+
+    def __init__(self):
+        import torch
+        self.torch = torch
+        self.code = (torch.uint8, torch.float8_e4m3fn)
+        self.scale = (torch.uint8, torch.float8_e8m0fnu)
+        self.value = (torch.bfloat16, torch.float32)
+        self.i32, self.bf16, self.f32 = (torch.int32,), (torch.bfloat16,), (torch.float32,)
+        self.dtype = {torch.bfloat16: DTYPE["bf16"], torch.float32: DTYPE["f32"],
+                      torch.uint8: DTYPE["e4m3"], torch.float8_e4m3fn: DTYPE["e4m3"]}
 
 
-def _fp8_types():
-    import torch
-    return ((torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.float8_e8m0fnu),
-            (torch.bfloat16, torch.float32), (torch.int32,))
+_fp8_types: Optional[_Fp8Types] = None
 
 
-def _value_dtype(t) -> int:
-    """DTYPE code of a tensor of values or codes."""
-    import torch
-    codes = {torch.bfloat16: DTYPE["bf16"], torch.float32: DTYPE["f32"],
-             torch.uint8: DTYPE["e4m3"], torch.float8_e4m3fn: DTYPE["e4m3"]}
-    if getattr(t, "dtype", None) not in codes:
-        raise TypeError(f"expected a bf16, fp32 or E4M3 tensor, got {getattr(t, 'dtype', type(t))}")
-    return codes[t.dtype]
+class _Fp8Call:
+    """Checks and converts the arguments of one call: a small call's time is mostly the host's."""
+    __slots__ = ("fn", "ty", "device")
+
+    def __init__(self, fn: str):
+        global _fp8_types
+        if _fp8_types is None:
+            _fp8_types = _Fp8Types()
+        self.fn = fn
+        self.ty = _fp8_types
+        cuda = self.ty.torch.cuda
+        self.device = cuda.current_device() if cuda.is_initialized() else 0
+
+    def __call__(self, name: str, t, dtypes, numel: int) -> Optional[int]:
+        if t is None or type(t) is int:
+            return t
+        if t.dtype not in dtypes:
+            raise TypeError(f"{self.fn}: {name} has dtype {t.dtype}, expected one of {dtypes}")
+        if t.numel() < numel:
+            raise ValueError(f"{self.fn}: {name} has {t.numel()} elements, needs {numel}")
+        if not t.is_contiguous():
+            raise ValueError(f"{self.fn}: {name} is not contiguous")
+        if t.get_device() != self.device:  # -1 for a host tensor
+            raise ValueError(f"{self.fn}: {name} is on {t.device}, not on the current CUDA device")
+        return t.data_ptr()
+
+    def stream(self, stream) -> Optional[int]:
+        return _stream(stream) if stream is not None else \
+            self.ty.torch._C._cuda_getCurrentRawStream(self.device)
+
+    def dtype(self, name: str, t) -> int:
+        """DTYPE code of a tensor of values or codes."""
+        code = self.ty.dtype.get(getattr(t, "dtype", None))
+        if code is None:
+            raise TypeError(f"{self.fn}: {name} must be a bf16, fp32 or E4M3 tensor, got "
+                            f"{getattr(t, 'dtype', type(t))}")
+        return code
 
 
 def moe_fp8_token_blocks(rows: int, E: int) -> int:
@@ -387,97 +413,94 @@ def moe_fp8_token_blocks(rows: int, E: int) -> int:
 
 def moe_quantize_fp8_block(x, rows: int, cols: int, q, scale, n_rows=None, stream=None) -> None:
     """E4M3 codes q [rows, cols] and E8M0 scales [rows, ceil(cols / 128)] of x (bf16 or fp32)."""
-    fn = "moe_quantize_fp8_block"
-    code, e8, val, i32 = _fp8_types()
-    _check(fn, load().moe_quantize_fp8_block(
-        _buffer(fn, "x", x, val, rows * cols), _value_dtype(x), rows, cols,
-        _buffer(fn, "n_rows", n_rows, i32, 1), _buffer(fn, "q", q, code, rows * cols),
-        _buffer(fn, "scale", scale, e8, rows * _nblocks(cols)), _stream(stream)))
+    buf = _Fp8Call("moe_quantize_fp8_block")
+    ty = buf.ty
+    _check(buf.fn, load().moe_quantize_fp8_block(
+        buf("x", x, ty.value, rows * cols), buf.dtype("x", x), rows, cols,
+        buf("n_rows", n_rows, ty.i32, 1), buf("q", q, ty.code, rows * cols),
+        buf("scale", scale, ty.scale, rows * _nblocks(cols)), buf.stream(stream)))
 
 
 def moe_quantize_fp8_weight(w, E: int, rows: int, cols: int, q, scale, q_t=None, scale_t=None,
                             stream=None) -> None:
     """Codes and scales of stacked weights w [E, rows, cols] in 128 x 128 blocks, and optionally of
     the transposed weights."""
-    fn = "moe_quantize_fp8_weight"
-    code, e8, val, _ = _fp8_types()
+    buf = _Fp8Call("moe_quantize_fp8_weight")
+    ty = buf.ty
     n, nb = E * rows * cols, E * _nblocks(rows) * _nblocks(cols)
-    _check(fn, load().moe_quantize_fp8_weight(
-        _buffer(fn, "w", w, val, n), _value_dtype(w), E, rows, cols,
-        _buffer(fn, "q", q, code, n), _buffer(fn, "scale", scale, e8, nb),
-        _buffer(fn, "q_t", q_t, code, n), _buffer(fn, "scale_t", scale_t, e8, nb),
-        _stream(stream)))
+    _check(buf.fn, load().moe_quantize_fp8_weight(
+        buf("w", w, ty.value, n), buf.dtype("w", w), E, rows, cols,
+        buf("q", q, ty.code, n), buf("scale", scale, ty.scale, nb),
+        buf("q_t", q_t, ty.code, n), buf("scale_t", scale_t, ty.scale, nb),
+        buf.stream(stream)))
 
 
 def moe_quantize_fp8_tokens(x, x_scale, rows: int, cols: int, offsets, E: int, q_t, scale_t,
                             stream=None) -> None:
     """Transposed codes q_t [cols, 128 B] and scales [B, cols] along each expert's rows, from bf16 or
     fp32 rows (x_scale None) or from E4M3 rows with their scales; B = moe_fp8_token_blocks."""
-    fn = "moe_quantize_fp8_tokens"
-    code, e8, val, i32 = _fp8_types()
+    buf = _Fp8Call("moe_quantize_fp8_tokens")
+    ty = buf.ty
     nb = moe_fp8_token_blocks(rows, E)
-    _check(fn, load().moe_quantize_fp8_tokens(
-        _buffer(fn, "x", x, val + code, rows * cols), _value_dtype(x),
-        _buffer(fn, "x_scale", x_scale, e8, rows * _nblocks(cols)), rows, cols,
-        _buffer(fn, "offsets", offsets, i32, E + 1), E,
-        _buffer(fn, "q_t", q_t, code, cols * BLOCK * nb),
-        _buffer(fn, "scale_t", scale_t, e8, nb * cols), _stream(stream)))
+    _check(buf.fn, load().moe_quantize_fp8_tokens(
+        buf("x", x, ty.value + ty.code, rows * cols), buf.dtype("x", x),
+        buf("x_scale", x_scale, ty.scale, rows * _nblocks(cols)), rows, cols,
+        buf("offsets", offsets, ty.i32, E + 1), E,
+        buf("q_t", q_t, ty.code, cols * BLOCK * nb),
+        buf("scale_t", scale_t, ty.scale, nb * cols), buf.stream(stream)))
 
 
 def moe_gemm_fp8_block(a, a_scale, rows: int, offsets, E: int, n: int, k: int, w, w_scale, out,
                        stream=None) -> None:
     """out [rows, n] (bf16 or fp32) = a [rows, k] w[e]^T, expert e's rows by offsets."""
-    fn = "moe_gemm_fp8_block"
-    code, e8, val, i32 = _fp8_types()
-    _check(fn, load().moe_gemm_fp8_block(
-        _buffer(fn, "a", a, code, rows * k), _buffer(fn, "a_scale", a_scale, e8, rows * _nblocks(k)),
-        rows, _buffer(fn, "offsets", offsets, i32, E + 1), E, n, k,
-        _buffer(fn, "w", w, code, E * n * k),
-        _buffer(fn, "w_scale", w_scale, e8, E * _nblocks(n) * _nblocks(k)),
-        _buffer(fn, "out", out, val, rows * n), _value_dtype(out), _stream(stream)))
+    buf = _Fp8Call("moe_gemm_fp8_block")
+    ty = buf.ty
+    _check(buf.fn, load().moe_gemm_fp8_block(
+        buf("a", a, ty.code, rows * k), buf("a_scale", a_scale, ty.scale, rows * _nblocks(k)),
+        rows, buf("offsets", offsets, ty.i32, E + 1), E, n, k,
+        buf("w", w, ty.code, E * n * k),
+        buf("w_scale", w_scale, ty.scale, E * _nblocks(n) * _nblocks(k)),
+        buf("out", out, ty.value, rows * n), buf.dtype("out", out), buf.stream(stream)))
 
 
 def moe_wgrad_fp8_block(a_t, a_scale, b_t, b_scale, rows: int, offsets, E: int, n: int, k: int, dw,
                         stream=None) -> None:
     """dw [E, n, k] (fp32) = per expert a^T b, both operands as moe_quantize_fp8_tokens wrote them."""
-    import torch
-    fn = "moe_wgrad_fp8_block"
-    code, e8, _, i32 = _fp8_types()
+    buf = _Fp8Call("moe_wgrad_fp8_block")
+    ty = buf.ty
     nb = moe_fp8_token_blocks(rows, E)
-    _check(fn, load().moe_wgrad_fp8_block(
-        _buffer(fn, "a_t", a_t, code, n * BLOCK * nb), _buffer(fn, "a_scale", a_scale, e8, nb * n),
-        _buffer(fn, "b_t", b_t, code, k * BLOCK * nb), _buffer(fn, "b_scale", b_scale, e8, nb * k),
-        rows, _buffer(fn, "offsets", offsets, i32, E + 1), E, n, k,
-        _buffer(fn, "dw", dw, (torch.float32,), E * n * k), _stream(stream)))
+    _check(buf.fn, load().moe_wgrad_fp8_block(
+        buf("a_t", a_t, ty.code, n * BLOCK * nb), buf("a_scale", a_scale, ty.scale, nb * n),
+        buf("b_t", b_t, ty.code, k * BLOCK * nb), buf("b_scale", b_scale, ty.scale, nb * k),
+        rows, buf("offsets", offsets, ty.i32, E + 1), E, n, k,
+        buf("dw", dw, ty.f32, E * n * k), buf.stream(stream)))
 
 
 def moe_swiglu_fp8_forward(gu, rows: int, ffn: int, h=None, h_q=None, h_scale=None, gu_q=None,
                            gu_scale=None, n_rows=None, stream=None) -> None:
     """h = silu(gate) * up of gu [rows, 2 ffn] in bf16 (h) and / or E4M3 (h_q, h_scale), and gu's own
     E4M3 checkpoint (gu_q, gu_scale)."""
-    import torch
-    fn = "moe_swiglu_fp8_forward"
-    code, e8, val, i32 = _fp8_types()
+    buf = _Fp8Call("moe_swiglu_fp8_forward")
+    ty = buf.ty
     n, nb = rows * ffn, rows * _nblocks(ffn)
-    _check(fn, load().moe_swiglu_fp8_forward(
-        _buffer(fn, "gu", gu, val, 2 * n), _value_dtype(gu), rows, ffn,
-        _buffer(fn, "n_rows", n_rows, i32, 1), _buffer(fn, "h", h, (torch.bfloat16,), n),
-        _buffer(fn, "h_q", h_q, code, n), _buffer(fn, "h_scale", h_scale, e8, nb),
-        _buffer(fn, "gu_q", gu_q, code, 2 * n), _buffer(fn, "gu_scale", gu_scale, e8, 2 * nb),
-        _stream(stream)))
+    _check(buf.fn, load().moe_swiglu_fp8_forward(
+        buf("gu", gu, ty.value, 2 * n), buf.dtype("gu", gu), rows, ffn,
+        buf("n_rows", n_rows, ty.i32, 1), buf("h", h, ty.bf16, n),
+        buf("h_q", h_q, ty.code, n), buf("h_scale", h_scale, ty.scale, nb),
+        buf("gu_q", gu_q, ty.code, 2 * n), buf("gu_scale", gu_scale, ty.scale, 2 * nb),
+        buf.stream(stream)))
 
 
 def moe_swiglu_fp8_backward(gu_q, gu_scale, dh, rows: int, ffn: int, dgu=None, dgu_q=None,
                             dgu_scale=None, h=None, n_rows=None, stream=None) -> None:
     """[d_gate | d_up] [rows, 2 ffn] in bf16 (dgu) and / or E4M3 (dgu_q, dgu_scale), and h again in
     bf16, from the checkpoint gu_q, gu_scale and dh [rows, ffn]."""
-    import torch
-    fn = "moe_swiglu_fp8_backward"
-    code, e8, val, i32 = _fp8_types()
+    buf = _Fp8Call("moe_swiglu_fp8_backward")
+    ty = buf.ty
     n, nb = rows * ffn, rows * _nblocks(ffn)
-    _check(fn, load().moe_swiglu_fp8_backward(
-        _buffer(fn, "gu_q", gu_q, code, 2 * n), _buffer(fn, "gu_scale", gu_scale, e8, 2 * nb),
-        _buffer(fn, "dh", dh, val, n), _value_dtype(dh), rows, ffn,
-        _buffer(fn, "n_rows", n_rows, i32, 1), _buffer(fn, "dgu", dgu, (torch.bfloat16,), 2 * n),
-        _buffer(fn, "dgu_q", dgu_q, code, 2 * n), _buffer(fn, "dgu_scale", dgu_scale, e8, 2 * nb),
-        _buffer(fn, "h", h, (torch.bfloat16,), n), _stream(stream)))
+    _check(buf.fn, load().moe_swiglu_fp8_backward(
+        buf("gu_q", gu_q, ty.code, 2 * n), buf("gu_scale", gu_scale, ty.scale, 2 * nb),
+        buf("dh", dh, ty.value, n), buf.dtype("dh", dh), rows, ffn,
+        buf("n_rows", n_rows, ty.i32, 1), buf("dgu", dgu, ty.bf16, 2 * n),
+        buf("dgu_q", dgu_q, ty.code, 2 * n), buf("dgu_scale", dgu_scale, ty.scale, 2 * nb),
+        buf("h", h, ty.bf16, n), buf.stream(stream)))

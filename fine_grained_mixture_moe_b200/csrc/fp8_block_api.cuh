@@ -20,6 +20,7 @@
   } while (0)
 
 static inline bool f8b_dtype(int32_t t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32; }
+static inline bool aligned32(const void *p) { return p && ((uintptr_t)p & 31u) == 0; }
 static inline bool aligned4(const void *p) { return p && ((uintptr_t)p & 3u) == 0; }
 
 moe_status_t moe_quantize_fp8_block(const void *in, int32_t in_dtype, int64_t rows, int32_t cols,
@@ -85,7 +86,7 @@ moe_status_t moe_gemm_fp8_block(const uint8_t *a, const uint8_t *a_scale, int64_
   if ((ceil_div(rows, 256) + (long long)E) * ceil_div(n, 256) > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
   MOE_REQUIRE(offsets || E == 1);
   if (rows == 0) return MOE_OK;
-  MOE_REQUIRE(aligned16(a) && a_scale && aligned16(w) && w_scale && aligned16(out) &&
+  MOE_REQUIRE(aligned16(a) && a_scale && aligned16(w) && w_scale && aligned32(out) &&
               (!offsets || aligned4(offsets)));
   F8Gemm p;
   std::memset(&p, 0, sizeof(p));
@@ -110,7 +111,7 @@ moe_status_t moe_wgrad_fp8_block(const uint8_t *a_t, const uint8_t *a_scale, con
   MOE_F8B_WIDTH(k);
   if (token_blocks(rows, E) > (1ll << 24) - 1) return MOE_ERR_UNSUPPORTED;  // K coordinates
   if ((long long)E * ceil_div(n, 256) * ceil_div(k, 256) > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
-  MOE_REQUIRE(aligned16(dw));
+  MOE_REQUIRE(aligned32(dw));
   cudaStream_t st = (cudaStream_t)stream;
   if (rows == 0)
     return cudaMemsetAsync(dw, 0, (size_t)E * n * k * sizeof(float), st) == cudaSuccess ? MOE_OK

@@ -3,14 +3,14 @@
 #pragma once
 
 // [rows, cols] bytes seen as {128 columns, rows, cols / 128 K blocks} (cols a multiple of 128): a
-// box {128, 128, 2} is the tiles of two K blocks, one after the other. Rows past the last, and the
+// box {128, box_rows, 2} is the tiles of two K blocks, one after the other. Rows past the last, and the
 // second K block past the last, read as zeros.
-bool make_map3_u8(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols) {
+bool make_map3_u8(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint32_t box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {128, rows, cols / 128};
   cuuint64_t strides[2] = {cols, 128};
-  cuuint32_t box[3] = {128, 128, 2};
+  cuuint32_t box[3] = {128, box_rows, 2};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(ptr), dims, strides,
                         box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -62,24 +62,26 @@ moe_status_t launch_gemm_fp8_block(F8Gemm &p, const uint8_t *a, const uint8_t *b
   const uint64_t lda = WGRAD ? (uint64_t)p.K * QB : (uint64_t)p.K;
   const uint64_t a_rows = WGRAD ? p.M : p.rows, b_rows = WGRAD ? (uint64_t)p.N : (uint64_t)p.E * p.N;
   if (WGRAD) p.K = (int)(lda / QB);
-  // two K blocks per copy when a row is whole K blocks (one 32 KB box instead of two copies) and
-  // the tile lists of E experts leave room for two such stages
-  p.kpb = lda % QB == 0 && f8g_stages(p.E, 2) >= 2 ? 2 : 1;
-  p.stages = f8g_stages(p.E, p.kpb);
-  static_assert(f8g_stages(1024, 1) >= 2, "tile lists of 1024 experts leave no room");
-  const bool ok = p.kpb == 2 ? make_map3_u8(&p.ma, a, a_rows, lda) && make_map3_u8(&p.mb, b, b_rows, lda)
-                             : make_map(&p.ma, a, a_rows, lda, 128, 1) &&
-                                   make_map(&p.mb, b, b_rows, lda, 128, 1);
+  p.tn = f8g_tile_n(p.N);
+  // two K blocks per copy when a row is whole K blocks (one box instead of two copies) and the tile
+  // lists of E experts leave room for two such stages
+  p.kpb = lda % QB == 0 && f8g_stages(p.E, p.tn, 2) >= 2 ? 2 : 1;
+  p.stages = f8g_stages(p.E, p.tn, p.kpb);
+  if (p.stages < F8G_SF_BUFS / p.kpb) return MOE_ERR_UNSUPPORTED;  // no tile width or E <= 1024 gives this
+  const uint32_t bb = p.tn / 2;
+  const bool ok = p.kpb == 2
+                      ? make_map3_u8(&p.ma, a, a_rows, lda, 128) && make_map3_u8(&p.mb, b, b_rows, lda, bb)
+                      : make_map(&p.ma, a, a_rows, lda, 128, 1) && make_map(&p.mb, b, b_rows, lda, bb, 1);
   if (!ok) return MOE_ERR_CUDA;
-  const size_t smem = f8g_smem_bytes(p.E, p.kpb);
+  const size_t smem = f8g_fixed_bytes(p.E) + (size_t)p.stages * f8g_stage_bytes(p.tn, p.kpb);
   auto kern = gemm_fp8_block_kernel<WGRAD>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return MOE_ERR_CUDA;
-  const long long tiles = WGRAD ? (long long)p.E * ceil_div(p.M, 256) * ceil_div(p.N, 256)
+  const long long tiles = WGRAD ? (long long)p.E * ceil_div(p.M, 256) * ceil_div(p.N, p.tn)
                                 : (ceil_div(p.rows, 256) + std::min<long long>(p.E, p.rows)) *
-                                      ceil_div(p.N, 256);
+                                      ceil_div(p.N, p.tn);
   const int pairs = (int)std::min<long long>(num_sms() / 2, tiles);
   const int kind = WGRAD ? K_F8B_WGRAD : K_F8B_GEMM;
   ProfScope ps(kind, st);
-  return launch_pdl(kern, dim3(2 * pairs), dim3(TC_THREADS), smem, st, p);
+  return launch_pdl(kern, dim3(2 * pairs), dim3(F8G_THREADS), smem, st, p);
 }

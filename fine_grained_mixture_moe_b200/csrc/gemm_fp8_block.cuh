@@ -8,20 +8,31 @@
 //   128 koff[g] .. 128 koff[g + 1] of a_t [n, pitch] and b_t [k, pitch],
 //   dw[g][r, c] = sum over its blocks tb of 2^(sa[tb, r] + sb[tb, c]) sum over t in tb of a_t b_t.
 //
-// The scales change with every 128 of K, so the tensor core sums one block at a time: four K = 32
-// instructions (kind::f8f6f4, products exact, fp32 sums) fill one of two 256-column TMEM buffers,
-// and the epilogue warps add the block, times its scales, into fp32 registers (128 columns of one
-// row per thread) while the other buffer fills. Powers of two make the scaling exact: the result
-// carries the rounding of fp32 sums only.
+// The scales are applied by the tensor core (kind::mxf8f6f4, block_scale): one E8M0 byte per row of
+// A and per row of B for each K = 32 instruction, read from TMEM. A block of 128 is four such
+// instructions with the same bytes. The fp32 accumulator of a tile stays in TMEM over the whole of
+// K and is read once; with the scales applied outside (a TMEM read and an fp32 multiply-add of every
+// element per block of K) the same tiles took 60 us instead of 27 on the Quartz gate|up product.
 //
-// Tiles, clusters and barriers are those of gemm_tc2.cuh: 256 x 256 per CTA pair, CTA r loads 128
-// rows of each operand, the leader issues M = 256, N = 256. A stage holds one or two K blocks of
-// 128 bytes (two by one 3-D box when K is a multiple of 128).
+// Clusters, stages and barriers are those of gemm_tc2.cuh: a tile of 256 x N (N = 16 .. 224) per CTA
+// pair, CTA r loads rows 128 r .. of the A tile and half of the N rows of B, the leader issues
+// M = 256 instructions. A stage holds one or two K blocks of 128 bytes (two by one 3-D box when K is a
+// multiple of 128). Warps: 0-3 write the scales to TMEM (one per lane quarter: the instruction
+// wants them in all four), 4-11 store finished tiles, 12 loads, 13 issues.
+// TMEM: accumulator b in columns 256 b .. 256 b + N; the 32 columns from 256 b + 224 hold two of the
+// four scale buffers (4 columns for 128 rows of A, up to 7 for N of B; 32 rows per column, one per lane,
+// the byte four times).
 #pragma once
 #include "fp8_block.cuh"
 #include "gemm_tc2.cuh"
 
 namespace moe {
+
+constexpr int F8G_N = 224;           // most columns of a tile
+constexpr int F8G_THREADS = 14 * 32;
+constexpr int F8G_STORE_WARPS = 8;
+constexpr int F8G_STG = F8G_STORE_WARPS * 4096;  // staging of 32 rows x 128 bytes per storing warp
+constexpr int F8G_SF_BUFS = 4;       // scale buffers of one K block
 
 struct F8Gemm {
   CUtensorMap ma, mb;
@@ -30,34 +41,36 @@ struct F8Gemm {
   void *out;
   long long rows;          // rows of a (gemm) or grouped rows (wgrad)
   int E, M, N, K;          // gemm: N = n, K = k; wgrad: M = n, N = k, K = blocks the buffers hold
+  int tn;                  // columns per tile, a multiple of 16 up to F8G_N
   int out_f32;
   int stages, kpb;
 };
 
+// Columns per tile: as few tiles as 224 columns allow, of about the same width.
+inline int f8g_tile_n(int n) {
+  const int tiles = (n + F8G_N - 1) / F8G_N;
+  return ((n + tiles - 1) / tiles + 15) / 16 * 16;
+}
+inline size_t f8g_fixed_bytes(int E) {
+  return 1024 + (size_t)F8G_STG + 256 + (size_t)(2 * E + 2 + F8G_THREADS / 32 + 1) * sizeof(int);
+}
+inline int f8g_stage_bytes(int tn, int kpb) { return (16384 + tn * 64) * kpb; }
+inline int f8g_stages(int E, int tn, int kpb) {
+  const long long n = (227LL * 1024 - (long long)f8g_fixed_bytes(E)) / f8g_stage_bytes(tn, kpb);
+  return n > 8 / kpb ? 8 / kpb : (int)n;
+}
+
 struct F8Tile {
   int g, m0, n0;
   int rows;         // rows of the group (gemm) or M (wgrad)
-  long long row0;   // its first row in a and out (gemm)
+  long long row0;   // its first row in a (gemm) and in out
   int kofs, nk;     // first K block and K blocks
 };
-
-constexpr int F8G_STAGE = 32768;  // one K block of both operands (this CTA's halves)
-constexpr int F8G_STG = TC_EPI_WARPS * 4096;
-constexpr size_t f8g_fixed_bytes(int E) {
-  return 1024 + (size_t)F8G_STG + 256 + (size_t)(2 * E + 2 + TC_THREADS / 32 + 1) * sizeof(int);
-}
-constexpr int f8g_stages(int E, int kpb) {
-  const long long n = (227LL * 1024 - (long long)f8g_fixed_bytes(E)) / ((long long)F8G_STAGE * kpb);
-  return n > 8 / kpb ? 8 / kpb : (int)n;
-}
-constexpr size_t f8g_smem_bytes(int E, int kpb) {
-  return f8g_fixed_bytes(E) + (size_t)f8g_stages(E, kpb) * F8G_STAGE * kpb;
-}
 
 // Tile counts per group scanned into prefix[0 .. E]; wgrad also the groups' K-block offsets.
 template <bool WGRAD>
 __device__ __forceinline__ int f8_tile_prefix(const F8Gemm &p, int *prefix, int *koff, int *tmp) {
-  const int nt = (p.N + 255) / 256;
+  const int nt = (p.N + p.tn - 1) / p.tn;
   for (int g = threadIdx.x; g < p.E; g += blockDim.x) {
     long long n = p.rows;
     if (p.offsets)
@@ -88,11 +101,11 @@ __device__ __forceinline__ F8Tile f8_decode(const F8Gemm &p, int tile, const int
     if (prefix[mid] <= tile) lo = mid;
     else hi = mid - 1;
   }
-  const int nt = (p.N + 255) / 256, local = tile - prefix[lo];
+  const int nt = (p.N + p.tn - 1) / p.tn, local = tile - prefix[lo];
   F8Tile t;
   t.g = lo;
   t.m0 = (local / nt) * 256;
-  t.n0 = (local % nt) * 256;
+  t.n0 = (local % nt) * p.tn;
   if (WGRAD) {
     t.rows = p.M;
     t.row0 = (long long)lo * p.M;
@@ -107,38 +120,51 @@ __device__ __forceinline__ F8Tile f8_decode(const F8Gemm &p, int tile, const int
   return t;
 }
 
-// 16 accumulator columns times their scales into the running sums.
-__device__ __forceinline__ void f8_fma16(float *acc, const uint32_t (&r)[16], float s) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = fmaf(__uint_as_float(r[i]), s, acc[i]);
+// One K = 32 step with the E8M0 scales of A and B at TMEM addresses sfa, sfb.
+__device__ __forceinline__ void f8_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+      ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
 }
-__device__ __forceinline__ void f8_fma16(float *acc, const uint32_t (&r)[16], float s, const float *col) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 c = *(const float4 *)(col + 4 * i);
-    acc[4 * i] = fmaf(__uint_as_float(r[4 * i]) * c.x, s, acc[4 * i]);
-    acc[4 * i + 1] = fmaf(__uint_as_float(r[4 * i + 1]) * c.y, s, acc[4 * i + 1]);
-    acc[4 * i + 2] = fmaf(__uint_as_float(r[4 * i + 2]) * c.z, s, acc[4 * i + 2]);
-    acc[4 * i + 3] = fmaf(__uint_as_float(r[4 * i + 3]) * c.w, s, acc[4 * i + 3]);
-  }
+__device__ __forceinline__ void tmem_st4(uint32_t addr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ bool f8_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                             uint64_t limit, long long info) {
+  bool ok = true;
+  if (!mbar_try_wait(bar, parity)) ok = mbar_wait(bar, parity, abort_flag, limit, info);
+  return __all_sync(0xffffffffu, ok);
 }
 
 template <bool WGRAD>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
     gemm_fp8_block_kernel(const __grid_constant__ F8Gemm p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int NST = p.stages, KPB = p.kpb;
-  const uint32_t stage_bytes = (uint32_t)F8G_STAGE * KPB, half_bytes = stage_bytes / 2;
-  constexpr uint32_t IDESC = (1u << 4) | (256u >> 3 << 17) | (256u >> 4 << 24);  // E4M3, fp32 sums
+  const int NST = p.stages, KPB = p.kpb, SFU = F8G_SF_BUFS / KPB;  // scale buffers in units of a stage
+  const uint32_t b_bytes = (uint32_t)p.tn * 64;                     // this CTA's half of B, one K block
+  const uint32_t a_stage = 16384u * KPB, stage_bytes = a_stage + b_bytes * KPB;
+  // E4M3 operands, E8M0 scales (byte 0 of a word), fp32 sums
+  const uint32_t IDESC = (1u << 23) | ((uint32_t)p.tn >> 3 << 17) | (256u >> 4 << 24);
 
   const uint32_t raw = smem_u32(smem_raw);
   unsigned char *base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   unsigned char *stg_all = base + (size_t)NST * stage_bytes;
   uint64_t *bars = (uint64_t *)(stg_all + F8G_STG);
-  uint32_t *tmem_slot = (uint32_t *)(bars + 2 * NST + 5);
+  uint32_t *tmem_slot = (uint32_t *)(bars + 2 * NST + 5 + F8G_SF_BUFS);
   volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
   int *prefix = (int *)(stg_all + F8G_STG + 256);
   int *koff = prefix + p.E + 1;
@@ -148,7 +174,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
   auto empty_bar = [&](int s) { return smem_u32(bars + NST + s); };
   auto accf_bar = [&](int b) { return smem_u32(bars + 2 * NST + b); };
   auto acce_bar = [&](int b) { return smem_u32(bars + 2 * NST + 2 + b); };
-  const uint32_t drain_bar = smem_u32(bars + 2 * NST + 4);
+  auto sff_bar = [&](int u) { return smem_u32(bars + 2 * NST + 4 + u); };
+  const uint32_t drain_bar = smem_u32(bars + 2 * NST + 4 + F8G_SF_BUFS);
 
   if (tid == 0) {
     for (int s = 0; s < NST; ++s) {
@@ -157,14 +184,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);
-      mbar_init(acce_bar(b), 2 * TC_EPI_WARPS);
+      mbar_init(acce_bar(b), 2 * F8G_STORE_WARPS);
     }
+    for (int u = 0; u < F8G_SF_BUFS; ++u) mbar_init(sff_bar(u), 2 * 4);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (warp == 1) {
+  if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),
                  "r"(512u)
@@ -181,8 +209,91 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const uint64_t limit = g_wait_limit_ns;
+  // scale buffer i (0 .. 3): 16 columns, 4 for A then up to 8 for B
+  auto sf_col = [&](int i) { return tmem_base + (uint32_t)(256 * (i >> 1) + F8G_N + 16 * (i & 1)); };
 
-  if (warp == 0) {
+  if (warp < 4) {
+    // ------------------------------------------------------------ scales (both CTAs)
+    // Unit i (the i-th stage's K blocks) uses scale buffers (i % SFU) KPB ..; its predecessor there,
+    // unit i - SFU, is done when the stage it used is released. That stage (NST >= SFU stages
+    // in turn) cannot be released again before unit i is written, so the parity is unambiguous.
+    const int nkb = (p.K + QB - 1) / QB, nnb = (p.N + QB - 1) / QB, nw = (p.tn + 31) / 32;
+    int tile = pair, kb = 0;
+    F8Tile t;
+    const uint8_t *pa[4];  // scales of rows 32 i + lane of this CTA's 128
+    bool oa[4];
+    auto enter = [&]() {
+      for (; tile < total; tile += npairs) {
+        t = f8_decode<WGRAD>(p, tile, prefix, koff);
+        if (t.nk > 0) break;
+      }
+      kb = 0;
+      if (tile >= total) return;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = t.m0 + (int)rank * 128 + 32 * i + lane;
+        oa[i] = r < t.rows;
+        pa[i] = WGRAD ? p.a_scale + (size_t)t.kofs * p.M + r : p.a_scale + (size_t)(t.row0 + r) * nkb;
+      }
+    };
+    uint32_t wa[2][4], wb[2][8];  // bytes of the next unit
+    auto fetch = [&]() {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int k = kb + j;
+        const bool on = j < KPB && k < t.nk;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          wa[j][i] = on && oa[i] ? __ldg(pa[i] + (WGRAD ? (size_t)k * p.M : (size_t)k)) : 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = t.n0 + 32 * i + lane;
+          wb[j][i] = !(on && i < nw && c < p.N) ? 0u
+                     : WGRAD ? __ldg(p.b_scale + (size_t)(t.kofs + k) * p.N + c)
+                             : __ldg(p.b_scale + ((size_t)t.g * nnb + c / QB) * nkb + k);
+        }
+      }
+    };
+    enter();
+    if (tile < total) fetch();
+    const uint32_t quarter = (uint32_t)(warp * 32) << 16;
+    int unit = 0, stage = 0;       // unit % SFU; the stage that unit i - SFU used
+    uint32_t phase = 0;
+    for (int i = 0; tile < total; ++i) {
+      uint32_t va[2][4], vb[2][8];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) va[j][x] = wa[j][x] * 0x01010101u;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) vb[j][x] = wb[j][x] * 0x01010101u;
+      }
+      const int used = min(KPB, t.nk - kb);
+      kb += KPB;
+      if (kb >= t.nk) {
+        tile += npairs;
+        enter();
+      }
+      if (tile < total) fetch();
+      if (i >= SFU) {
+        if (!f8_wait_warp(empty_bar(stage), phase, abort_flag, limit, INFO_WAIT_MMA_EMPTY)) break;
+        if (++stage == NST) { stage = 0; phase ^= 1u; }
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (j < used) {
+          const uint32_t at = sf_col(unit * KPB + j) + quarter;
+          tmem_st4(at, va[j]);
+          tmem_st8(at + 4, vb[j]);
+        }
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta0(sff_bar(unit));
+      if (++unit == SFU) unit = 0;
+    }
+  } else if (warp == 12) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
     if (lane == 0) {
       int stage = 0;
@@ -193,15 +304,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
         const F8Tile t = f8_decode<WGRAD>(p, tile, prefix, koff);
         // CTA 1's 128 rows may hold none of the group: never stored, so not loaded (gemm_tc2.cuh)
         const bool a1_void = t.m0 + 128 >= t.rows;
-        const uint32_t tx = 2 * stage_bytes - (a1_void ? half_bytes : 0);
+        const uint32_t tx = 2 * stage_bytes - (a1_void ? a_stage : 0);
         const int a_row = (WGRAD ? 0 : (int)t.row0) + t.m0 + (int)rank * 128;
-        const int b_row = (WGRAD ? 0 : t.g * p.N) + t.n0 + (int)rank * 128;
+        const int b_row = (WGRAD ? 0 : t.g * p.N) + t.n0 + (int)rank * (p.tn / 2);
         for (int kb = 0; kb < t.nk; kb += KPB) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, limit, INFO_WAIT_MMA_EMPTY)) {
             ok = false;
             break;
           }
-          const uint32_t sA = smem_u32(base + (size_t)stage * stage_bytes), sB = sA + half_bytes;
+          const uint32_t sA = smem_u32(base + (size_t)stage * stage_bytes), sB = sA + a_stage;
           if (rank == 0) mbar_expect_tx(full_bar(stage), tx);
           if (KPB == 2) {
             if (rank == 0 || !a1_void)
@@ -226,41 +337,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 13) {
     // ------------------------------------------------------------ MMA issuer (leader only)
     if (rank == 0 && lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int acc = 0;
-      uint32_t acc_phase = 0;
+      int stage = 0, acc = 0, unit = 0;
+      uint32_t phase = 0, acc_phase = 0, unit_phase = 0;
       bool ok = true, any = false;
       for (int tile = pair; tile < total && ok; tile += npairs) {
         const F8Tile t = f8_decode<WGRAD>(p, tile, prefix, koff);
-        for (int kb = 0; kb < t.nk && ok; kb += KPB) {
-          if (!mbar_wait(full_bar(stage), phase, abort_flag, limit, INFO_WAIT_TMA_FULL)) {
+        if (t.nk == 0) continue;
+        if (!mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag, limit, INFO_WAIT_ACC_EMPTY)) {
+          ok = false;
+          break;
+        }
+        const uint32_t d = tmem_base + (uint32_t)(acc * 256);
+        for (int kb = 0; kb < t.nk; kb += KPB) {
+          if (!mbar_wait(sff_bar(unit), unit_phase, abort_flag, limit, INFO_WAIT_TMA_FULL) ||
+              !mbar_wait(full_bar(stage), phase, abort_flag, limit, INFO_WAIT_TMA_FULL)) {
             ok = false;
             break;
           }
-          const uint32_t sA0 = smem_u32(base + (size_t)stage * stage_bytes), sB0 = sA0 + half_bytes;
+          tc_fence_after();
+          const uint32_t sA0 = smem_u32(base + (size_t)stage * stage_bytes), sB0 = sA0 + a_stage;
           for (int j = 0; j < KPB && kb + j < t.nk; ++j) {
-            if (!mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag, limit, INFO_WAIT_ACC_EMPTY)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t d = tmem_base + (uint32_t)(acc * 256);
-            const uint32_t sA = sA0 + j * 16384, sB = sB0 + j * 16384;
+            const uint32_t sf = sf_col(unit * KPB + j);
+            const uint32_t sA = sA0 + j * 16384, sB = sB0 + j * b_bytes;
 #pragma unroll
             for (int k32 = 0; k32 < 4; ++k32)
-              tc2_mma_f8(d, make_sdesc(sA + k32 * 32), make_sdesc(sB + k32 * 32), IDESC, k32 > 0);
-            any = true;
-            tc2_commit_both(accf_bar(acc));
-            if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+              f8_mma(d, make_sdesc(sA + k32 * 32), make_sdesc(sB + k32 * 32), IDESC, sf, sf + 4,
+                     kb > 0 || j > 0 || k32 > 0);
           }
-          if (!ok) break;
+          any = true;
           tc2_commit_both(empty_bar(stage));
           if (++stage == NST) { stage = 0; phase ^= 1u; }
+          if (++unit == SFU) { unit = 0; unit_phase ^= 1u; }
         }
+        if (!ok) break;
+        tc2_commit_both(accf_bar(acc));
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
       if (!ok && any) {
         tc2_commit_both(drain_bar);
@@ -270,121 +384,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ accumulate and store (warps 2..9)
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    unsigned char *stg = stg_all + (warp - 2) * 4096;
-    int acc_buf = 0;
+    // ------------------------------------------------------------ store (warps 4 .. 11)
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    unsigned char *stg = stg_all + (warp - 4) * 4096;
+    const int ebytes = p.out_f32 ? 4 : 2, cpp = 128 / ebytes;  // columns per pass: 128 bytes of a row
+    int acc = 0;
     uint32_t acc_phase = 0;
-    const int nkb = (p.K + QB - 1) / QB, nnb = (p.N + QB - 1) / QB;
     for (int tile = pair; tile < total; tile += npairs) {
       const F8Tile t = f8_decode<WGRAD>(p, tile, prefix, koff);
-      const int rbase = t.m0 + (int)rank * 128 + q * 32, row = rbase + lane;
-      const int col0 = t.n0 + half * 128;
-      const bool live = rbase < t.rows && col0 < p.N;  // this warp stores something
-      const bool row_ok = live && row < t.rows;
-      // the row's scales: one byte per K block; wgrad: the 128 columns' scales too, 4 per lane
-      const uint8_t *sa = nullptr, *sb = nullptr;
-      if (WGRAD) {
-        sa = p.a_scale + (size_t)t.kofs * p.M + row;
-        sb = p.b_scale + (size_t)t.kofs * p.N + col0 + 4 * lane;
-      } else {
-        sa = p.a_scale + (size_t)(t.row0 + row) * nkb;
-        sb = p.b_scale + ((size_t)t.g * nnb + col0 / QB) * nkb;
-      }
-      const bool col_ok = live && (!WGRAD || col0 + 4 * lane < p.N);
-      float acc[128];
-#pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-      bool ok = true;
-      for (int kb = 0; kb < t.nk; ++kb) {
-        uint32_t ba = 0, bb = 0;
-        if (row_ok) ba = __ldg(sa + (size_t)kb * (WGRAD ? p.M : 1));
-        if (col_ok) bb = WGRAD ? __ldg((const uint32_t *)(sb + (size_t)kb * p.N)) : __ldg(sb + kb);
-        float s = e8m0_value(ba);
-        const float *cs = (const float *)stg + (kb & 1) * 128;
-        if (WGRAD) {
-          *(float4 *)(stg + (kb & 1) * 512 + lane * 16) =
-              make_float4(e8m0_value(bb & 255u), e8m0_value(bb >> 8 & 255u),
-                          e8m0_value(bb >> 16 & 255u), e8m0_value(bb >> 24));
-          __syncwarp();
-        } else {
-          s *= e8m0_value(bb);
-        }
-        if (!mbar_try_wait(accf_bar(acc_buf), acc_phase))
-          ok = mbar_wait(accf_bar(acc_buf), acc_phase, abort_flag, limit, INFO_WAIT_ACC_FULL);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+      const int rbase = t.m0 + (int)rank * 128 + q * 32;
+      const int nrows = min(32, t.rows - rbase), ncols = min(p.tn, p.N - t.n0);
+      if (t.nk > 0) {
+        if (!f8_wait_warp(accf_bar(acc), acc_phase, abort_flag, limit, INFO_WAIT_ACC_FULL)) break;
         tc_fence_after();
-        if (live) {
-          const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc_buf * 256 + half * 128);
-          uint32_t r0[16], r1[16];
-          tmem_ld16(tb, r0);
-#pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            tmem_wait_ld();
-            tmem_ld16(tb + c + 16, r1);
-            if (WGRAD) f8_fma16(acc + c, r0, s, cs + c);
-            else f8_fma16(acc + c, r0, s);
-            tmem_wait_ld();
-            if (c + 32 < 128) tmem_ld16(tb + c + 32, r0);
-            if (c + 32 == 128) {  // the buffer is read: the next block may fill it
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cta0(acce_bar(acc_buf));
-            }
-            if (WGRAD) f8_fma16(acc + c + 16, r1, s, cs + c + 16);
-            else f8_fma16(acc + c + 16, r1, s);
-          }
-        } else {
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cta0(acce_bar(acc_buf));
-        }
-        if (++acc_buf == 2) { acc_buf = 0; acc_phase ^= 1u; }
       }
-      if (!ok) break;
-      if (!live) continue;
-      // 32 rows x 128 bytes at a time through the warp's staging buffer: lane = row in, then 8
-      // lanes per row out (whole 128-byte lines)
-      __syncwarp();
-      const int ebytes = p.out_f32 ? 4 : 2, cpp = 128 / ebytes;  // columns per pass
-      unsigned char *out = (unsigned char *)p.out + ((size_t)(t.row0 + rbase) * p.N + col0) * ebytes;
+      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
+      unsigned char *out = (unsigned char *)p.out + ((size_t)(t.row0 + rbase) * p.N + t.n0) * ebytes;
       const size_t pitch = (size_t)p.N * ebytes;
-      const int nrows = min(32, t.rows - rbase), ncols = min(128, p.N - col0);
-      auto flush = [&](int c) {
-        __syncwarp();
+      // the two warps of a lane quarter take every other pass: 32 rows of the staging buffer, written
+      // lane = row, read 8 lanes per row (whole 128-byte lines)
+      if (nrows > 0)
+        for (int c = half * cpp; c < ncols; c += 2 * cpp) {
+          if (p.out_f32) {
+            uint32_t r[32];
+            if (t.nk > 0) {
+              tmem_ld32(tb + c, r);
+              tmem_wait_ld();
+            } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = 4 * i + (lane >> 3), ch = lane & 7;
-          if (rr < nrows && c + ch * (cpp >> 3) < ncols)
-            *(uint4 *)(out + rr * pitch + (size_t)c * ebytes + ch * 16) =
-                *(const uint4 *)(stg + rr * 128 + ((ch ^ (rr & 7)) << 4));
-        }
-        __syncwarp();
-      };
-      if (p.out_f32) {
+              for (int i = 0; i < 32; ++i) r[i] = 0u;
+            }
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
+            for (int i = 0; i < 8; ++i)
+              *(uint4 *)(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                  make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+          } else {
+            uint32_t r[64];
+            tmem_ld32(tb + c, *(uint32_t(*)[32])r);
+            tmem_ld32(tb + c + 32, *(uint32_t(*)[32])(r + 32));
+            tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *(float4 *)(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) =
-                make_float4(acc[c + 4 * i], acc[c + 4 * i + 1], acc[c + 4 * i + 2], acc[c + 4 * i + 3]);
-          flush(c);
-        }
-      } else {
+            for (int i = 0; i < 8; ++i) {
+              uint32_t w[4];
 #pragma unroll
-        for (int c = 0; c < 128; c += 64) {
+              for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[8 * i + 2 * j]),
+                                                               __uint_as_float(r[8 * i + 2 * j + 1]));
+                w[j] = *(const uint32_t *)&v;
+              }
+              *(uint4 *)(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(acc[c + 8 * i + 2 * j], acc[c + 8 * i + 2 * j + 1]);
-              w[j] = *(const uint32_t *)&b;
-            }
-            *(uint4 *)(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            const int rr = 4 * i + (lane >> 3), ch = lane & 7;
+            if (rr < nrows && c + ch * (cpp >> 3) < ncols)
+              *(uint4 *)(out + rr * pitch + (size_t)c * ebytes + ch * 16) =
+                  *(const uint4 *)(stg + rr * 128 + ((ch ^ (rr & 7)) << 4));
           }
-          flush(c);
+          __syncwarp();
         }
+      if (t.nk > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cta0(acce_bar(acc));
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
     }
   }
@@ -392,7 +457,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // no CTA leaves while its peer may still read its smem or TMEM
-  if (warp == 1) {
+  if (warp == 13) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u)
                  : "memory");

@@ -396,7 +396,7 @@ moe_status_t moe_quantize_fp8_tokens(const void *in, int32_t in_dtype, const uin
 /* Grouped product: for rows r of expert e, with the values the codes stand for,
  *   out[r, c] = sum_i a[r, i] w[e, c, i],  c < n, i < k
  * a, a_scale: rows layout [rows, k]; w, w_scale: weight layout [E, n, k]; out [rows, n] in bf16 or
- * fp32 (out_dtype), rounded once from fp32 sums. The input gradient is the same call on the
+ * fp32 (out_dtype; 32-byte aligned), rounded once from fp32 sums. The input gradient is the same call on the
  * transposed weights. offsets may be NULL with E = 1: one weight for all rows. Rows outside every
  * expert are not written. */
 moe_status_t moe_gemm_fp8_block(const uint8_t *a, const uint8_t *a_scale, int64_t rows,
@@ -405,8 +405,8 @@ moe_status_t moe_gemm_fp8_block(const uint8_t *a, const uint8_t *a_scale, int64_
                                 int32_t out_dtype, void *stream);
 
 /* Weight gradient: dw[e, c, i] = sum over the rows r of expert e of a[r, c] b[r, i], c < n, i < k
- * (a the product's upstream gradient, b its input), fp32 [E, n, k]; zeros for an expert with no
- * rows. a_t, a_scale: tokens layout of [rows, n]; b_t, b_scale: of [rows, k] (b_scale 4-byte
+ * (a the product's upstream gradient, b its input), fp32 [E, n, k], 32-byte aligned; zeros for an
+ * expert with no rows. a_t, a_scale: tokens layout of [rows, n]; b_t, b_scale: of [rows, k] (b_scale 4-byte
  * aligned), both made with these rows, offsets and E. */
 moe_status_t moe_wgrad_fp8_block(const uint8_t *a_t, const uint8_t *a_scale, const uint8_t *b_t,
                                  const uint8_t *b_scale, int64_t rows, const int32_t *offsets,
