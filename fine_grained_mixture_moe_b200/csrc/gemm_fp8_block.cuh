@@ -5,7 +5,7 @@
 //   out[r, c] = sum over 128-wide blocks kb of 2^(sa[r, kb] + sw[g, c / 128, kb])
 //               * sum over k in kb of a[r, k] w[g, c, k]
 // wgrad (WGRAD = true): both operands are transposed and K is the token: expert g owns the columns
-//   128 koff[g] .. 128 koff[g + 1] of a_t [n, pitch] and b_t [k, pitch],
+//   128 start[g] .. 128 start[g + 1] of a_t [n, pitch] and b_t [k, pitch],
 //   dw[g][r, c] = sum over its blocks tb of 2^(sa[tb, r] + sb[tb, c]) sum over t in tb of a_t b_t.
 //
 // The scales are applied by the tensor core (kind::mxf8f6f4, block_scale): one E8M0 byte per row of
@@ -67,25 +67,28 @@ struct F8Tile {
   int kofs, nk;     // first K block and K blocks
 };
 
-// Tile counts per group scanned into prefix[0 .. E]; wgrad also the groups' K-block offsets.
+// Tile counts per group scanned into prefix[0 .. E], and in start[0 .. E] the groups' first rows
+// (gemm) or first K blocks (wgrad).
 template <bool WGRAD>
-__device__ __forceinline__ int f8_tile_prefix(const F8Gemm &p, int *prefix, int *koff, int *tmp) {
+__device__ __forceinline__ int f8_tile_prefix(const F8Gemm &p, int *prefix, int *start, int *tmp) {
   const int nt = (p.N + p.tn - 1) / p.tn;
-  for (int g = threadIdx.x; g < p.E; g += blockDim.x) {
-    long long n = p.rows;
-    if (p.offsets)
-      n = max(expert_bound(p.offsets, g + 1, p.rows) - expert_bound(p.offsets, g, p.rows), 0ll);
+  for (int g = threadIdx.x; g <= p.E; g += blockDim.x) {
+    const long long a = p.offsets ? expert_bound(p.offsets, g, p.rows) : g ? p.rows : 0;
+    long long n = 0;
+    if (g < p.E)
+      n = max((p.offsets ? expert_bound(p.offsets, g + 1, p.rows) : p.rows) - a, 0ll);
     if (WGRAD) {
       prefix[g] = ((p.M + 255) / 256) * nt;
-      koff[g] = (int)((n + QB - 1) / QB);
+      start[g] = (int)((n + QB - 1) / QB);
     } else {
       prefix[g] = (int)((n + 255) / 256) * nt;
+      start[g] = (int)a;
     }
   }
   __syncthreads();
   if (WGRAD) {
-    const int all = block_excl_scan_inplace(koff, p.E, tmp);
-    if (threadIdx.x == 0) koff[p.E] = all;
+    const int all = block_excl_scan_inplace(start, p.E, tmp);
+    if (threadIdx.x == 0) start[p.E] = all;
   }
   const int total = block_excl_scan_inplace(prefix, p.E, tmp);
   if (threadIdx.x == 0) prefix[p.E] = total;
@@ -93,27 +96,39 @@ __device__ __forceinline__ int f8_tile_prefix(const F8Gemm &p, int *prefix, int 
   return total;
 }
 
-template <bool WGRAD>
-__device__ __forceinline__ F8Tile f8_decode(const F8Gemm &p, int tile, const int *prefix, const int *koff) {
+// The group of a tile, and its K blocks (all that the issuing warp needs).
+__device__ __forceinline__ int f8_group(const F8Gemm &p, int tile, const int *prefix) {
   int lo = 0, hi = p.E - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (prefix[mid] <= tile) lo = mid;
     else hi = mid - 1;
   }
-  const int nt = (p.N + p.tn - 1) / p.tn, local = tile - prefix[lo];
+  return lo;
+}
+template <bool WGRAD>
+__device__ __forceinline__ int f8_blocks(const F8Gemm &p, int tile, const int *prefix, const int *start) {
+  if (!WGRAD) return (p.K + QB - 1) / QB;
+  const int g = f8_group(p, tile, prefix);
+  return min(start[g + 1], p.K) - min(start[g], p.K);
+}
+
+template <bool WGRAD>
+__device__ __forceinline__ F8Tile f8_decode(const F8Gemm &p, int tile, const int *prefix, const int *start) {
+  const int nt = (p.N + p.tn - 1) / p.tn;
   F8Tile t;
-  t.g = lo;
+  t.g = f8_group(p, tile, prefix);
+  const int local = tile - prefix[t.g];
   t.m0 = (local / nt) * 256;
   t.n0 = (local % nt) * p.tn;
   if (WGRAD) {
     t.rows = p.M;
-    t.row0 = (long long)lo * p.M;
-    t.kofs = min(koff[lo], p.K);
-    t.nk = min(koff[lo + 1], p.K) - t.kofs;
+    t.row0 = (long long)t.g * p.M;
+    t.kofs = min(start[t.g], p.K);
+    t.nk = min(start[t.g + 1], p.K) - t.kofs;
   } else {
-    t.row0 = p.offsets ? expert_bound(p.offsets, lo, p.rows) : 0;
-    t.rows = (int)((p.offsets ? expert_bound(p.offsets, lo + 1, p.rows) : p.rows) - t.row0);
+    t.row0 = start[t.g];
+    t.rows = start[t.g + 1] - start[t.g];
     t.kofs = 0;
     t.nk = (p.K + QB - 1) / QB;
   }
@@ -164,29 +179,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
   unsigned char *base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   unsigned char *stg_all = base + (size_t)NST * stage_bytes;
   uint64_t *bars = (uint64_t *)(stg_all + F8G_STG);
-  uint32_t *tmem_slot = (uint32_t *)(bars + 2 * NST + 5 + F8G_SF_BUFS);
+  uint32_t *tmem_slot = (uint32_t *)(bars + 2 * NST + 5);
   volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
   int *prefix = (int *)(stg_all + F8G_STG + 256);
-  int *koff = prefix + p.E + 1;
-  int *scan_tmp = koff + p.E + 1;
+  int *start = prefix + p.E + 1;
+  int *scan_tmp = start + p.E + 1;
 
   auto full_bar = [&](int s) { return smem_u32(bars + s); };
   auto empty_bar = [&](int s) { return smem_u32(bars + NST + s); };
   auto accf_bar = [&](int b) { return smem_u32(bars + 2 * NST + b); };
   auto acce_bar = [&](int b) { return smem_u32(bars + 2 * NST + 2 + b); };
-  auto sff_bar = [&](int u) { return smem_u32(bars + 2 * NST + 4 + u); };
-  const uint32_t drain_bar = smem_u32(bars + 2 * NST + 4 + F8G_SF_BUFS);
+  const uint32_t drain_bar = smem_u32(bars + 2 * NST + 4);
 
   if (tid == 0) {
     for (int s = 0; s < NST; ++s) {
-      mbar_init(full_bar(s), 1);
+      mbar_init(full_bar(s), 1 + 2 * 4);  // the operands' bytes, and the scale warps of both CTAs
       mbar_init(empty_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);
       mbar_init(acce_bar(b), 2 * F8G_STORE_WARPS);
     }
-    for (int u = 0; u < F8G_SF_BUFS; ++u) mbar_init(sff_bar(u), 2 * 4);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -203,7 +216,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
   griddep_wait();
   stamp.started();
   griddep_launch();
-  const int total = f8_tile_prefix<WGRAD>(p, prefix, koff, scan_tmp);
+  const int total = f8_tile_prefix<WGRAD>(p, prefix, start, scan_tmp);
   tc_fence_before();
   cluster_sync_all();  // barriers of both CTAs initialised, TMEM allocated in both
   tc_fence_after();
@@ -224,7 +237,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
     bool oa[4];
     auto enter = [&]() {
       for (; tile < total; tile += npairs) {
-        t = f8_decode<WGRAD>(p, tile, prefix, koff);
+        t = f8_decode<WGRAD>(p, tile, prefix, start);
         if (t.nk > 0) break;
       }
       kb = 0;
@@ -257,7 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
     enter();
     if (tile < total) fetch();
     const uint32_t quarter = (uint32_t)(warp * 32) << 16;
-    int unit = 0, stage = 0;       // unit % SFU; the stage that unit i - SFU used
+    int unit = 0, mine = 0, stage = 0;  // i % SFU; i's stage; the stage that unit i - SFU used
     uint32_t phase = 0;
     for (int i = 0; tile < total; ++i) {
       uint32_t va[2][4], vb[2][8];
@@ -290,7 +303,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cta0(sff_bar(unit));
+      if (lane == 0) mbar_arrive_cta0(full_bar(mine));
+      if (++mine == NST) mine = 0;
       if (++unit == SFU) unit = 0;
     }
   } else if (warp == 12) {
@@ -301,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
       bool ok = true;
       uint32_t issued = 0, issued_parity = 0;  // bit s: stage s was filled, with that parity
       for (int tile = pair; tile < total && ok; tile += npairs) {
-        const F8Tile t = f8_decode<WGRAD>(p, tile, prefix, koff);
+        const F8Tile t = f8_decode<WGRAD>(p, tile, prefix, start);
         // CTA 1's 128 rows may hold none of the group: never stored, so not loaded (gemm_tc2.cuh)
         const bool a1_void = t.m0 + 128 >= t.rows;
         const uint32_t tx = 2 * stage_bytes - (a1_void ? a_stage : 0);
@@ -340,37 +354,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
   } else if (warp == 13) {
     // ------------------------------------------------------------ MMA issuer (leader only)
     if (rank == 0 && lane == 0) {
+      // the tensor core drains its queue in a few hundred cycles: between two stages this thread does
+      // one inlined barrier test, and the descriptors are kept as running values
       int stage = 0, acc = 0, unit = 0;
-      uint32_t phase = 0, acc_phase = 0, unit_phase = 0;
+      uint32_t phase = 0, acc_phase = 0;
       bool ok = true, any = false;
+      const uint64_t adesc0 = make_sdesc(smem_u32(base)), bdesc0 = make_sdesc(smem_u32(base) + a_stage);
+      int nk = pair < total ? f8_blocks<WGRAD>(p, pair, prefix, start) : 0;
       for (int tile = pair; tile < total && ok; tile += npairs) {
-        const F8Tile t = f8_decode<WGRAD>(p, tile, prefix, koff);
-        if (t.nk == 0) continue;
-        if (!mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag, limit, INFO_WAIT_ACC_EMPTY)) {
+        const int left0 = nk;
+        nk = tile + npairs < total ? f8_blocks<WGRAD>(p, tile + npairs, prefix, start) : 0;
+        if (left0 == 0) continue;
+        if (!mbar_try_wait(acce_bar(acc), acc_phase ^ 1u) &&
+            !mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag, limit, INFO_WAIT_ACC_EMPTY)) {
           ok = false;
           break;
         }
         const uint32_t d = tmem_base + (uint32_t)(acc * 256);
-        for (int kb = 0; kb < t.nk; kb += KPB) {
-          if (!mbar_wait(sff_bar(unit), unit_phase, abort_flag, limit, INFO_WAIT_TMA_FULL) ||
+        uint32_t accumulate = 0;
+        for (int left = left0; left > 0; left -= KPB) {
+          if (!mbar_try_wait(full_bar(stage), phase) &&
               !mbar_wait(full_bar(stage), phase, abort_flag, limit, INFO_WAIT_TMA_FULL)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sA0 = smem_u32(base + (size_t)stage * stage_bytes), sB0 = sA0 + a_stage;
-          for (int j = 0; j < KPB && kb + j < t.nk; ++j) {
-            const uint32_t sf = sf_col(unit * KPB + j);
-            const uint32_t sA = sA0 + j * 16384, sB = sB0 + j * b_bytes;
+          const uint64_t off = (uint64_t)(((uint32_t)stage * stage_bytes) >> 4);
+          uint64_t ad = adesc0 + off, bd = bdesc0 + off;
+          uint32_t sf = sf_col(unit * KPB);
+          for (int j = 0; j < min(KPB, left); ++j) {
 #pragma unroll
-            for (int k32 = 0; k32 < 4; ++k32)
-              f8_mma(d, make_sdesc(sA + k32 * 32), make_sdesc(sB + k32 * 32), IDESC, sf, sf + 4,
-                     kb > 0 || j > 0 || k32 > 0);
+            for (int k32 = 0; k32 < 4; ++k32) {  // 32 bytes of K: two 16-byte units further
+              f8_mma(d, ad + 2 * k32, bd + 2 * k32, IDESC, sf, sf + 4, accumulate);
+              accumulate = 1;
+            }
+            ad += 16384 >> 4;
+            bd += b_bytes >> 4;
+            sf += 16;  // the two K blocks of a stage use neighbouring scale buffers
           }
           any = true;
           tc2_commit_both(empty_bar(stage));
           if (++stage == NST) { stage = 0; phase ^= 1u; }
-          if (++unit == SFU) { unit = 0; unit_phase ^= 1u; }
+          if (++unit == SFU) unit = 0;
         }
         if (!ok) break;
         tc2_commit_both(accf_bar(acc));
@@ -391,7 +416,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int tile = pair; tile < total; tile += npairs) {
-      const F8Tile t = f8_decode<WGRAD>(p, tile, prefix, koff);
+      const F8Tile t = f8_decode<WGRAD>(p, tile, prefix, start);
       const int rbase = t.m0 + (int)rank * 128 + q * 32;
       const int nrows = min(32, t.rows - rbase), ncols = min(p.tn, p.N - t.n0);
       if (t.nk > 0) {
