@@ -67,7 +67,6 @@ moe_status_t launch_gemm_fp8_block(F8Gemm &p, const uint8_t *a, const uint8_t *b
   // lists of E experts leave room for two such stages
   p.kpb = lda % QB == 0 && f8g_stages(p.E, p.tn, 2) >= 2 ? 2 : 1;
   p.stages = f8g_stages(p.E, p.tn, p.kpb);
-  if (p.stages < F8G_SF_BUFS / p.kpb) return MOE_ERR_UNSUPPORTED;  // no tile width or E <= 1024 gives this
   const uint32_t bb = p.tn / 2;
   const bool ok = p.kpb == 2
                       ? make_map3_u8(&p.ma, a, a_rows, lda, 128) && make_map3_u8(&p.mb, b, b_rows, lda, bb)

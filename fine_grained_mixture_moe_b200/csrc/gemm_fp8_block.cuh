@@ -9,8 +9,9 @@
 //   dw[g][r, c] = sum over its blocks tb of 2^(sa[tb, r] + sb[tb, c]) sum over t in tb of a_t b_t.
 //
 // The scales are applied by the tensor core (kind::mxf8f6f4, block_scale): one E8M0 byte per row of
-// A and per row of B for each K = 32 instruction, read from TMEM. A block of 128 is four such
-// instructions with the same bytes. The fp32 accumulator of a tile stays in TMEM over the whole of
+// A and per row of B for each K = 32 instruction, read from TMEM. A TMEM word holds four bytes and the
+// instruction names one of them, so a word serves four blocks of 128, and the four instructions of a
+// block name the same byte. The fp32 accumulator of a tile stays in TMEM over the whole of
 // K and is read once; with the scales applied outside (a TMEM read and an fp32 multiply-add of every
 // element per block of K) the same tiles took 60 us instead of 27 on the Quartz gate|up product.
 //
@@ -20,8 +21,9 @@
 // multiple of 128). Warps: 0-3 write the scales to TMEM (one per lane quarter: the instruction
 // wants them in all four), 4-11 store finished tiles, 12 loads, 13 issues.
 // TMEM: accumulator b in columns 256 b .. 256 b + N; the 32 columns from 256 b + 224 hold two of the
-// four scale buffers (4 columns for 128 rows of A, up to 7 for N of B; 32 rows per column, one per lane,
-// the byte four times).
+// four scale buffers, each for four blocks of K (4 columns for 128 rows of A, up to 7 for N of B; 32
+// rows per column, one per lane). With one block per buffer the tensor core waited for its scales:
+// 42 us on the Quartz gate|up product.
 #pragma once
 #include "fp8_block.cuh"
 #include "gemm_tc2.cuh"
@@ -32,7 +34,8 @@ constexpr int F8G_N = 224;           // most columns of a tile
 constexpr int F8G_THREADS = 14 * 32;
 constexpr int F8G_STORE_WARPS = 8;
 constexpr int F8G_STG = F8G_STORE_WARPS * 4096;  // staging of 32 rows x 128 bytes per storing warp
-constexpr int F8G_SF_BUFS = 4;       // scale buffers of one K block
+constexpr int F8G_SF_BUFS = 4;       // scale buffers ...
+constexpr int F8G_SF_K = 4;          // ... of four K blocks
 
 struct F8Gemm {
   CUtensorMap ma, mb;
@@ -169,17 +172,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int NST = p.stages, KPB = p.kpb, SFU = F8G_SF_BUFS / KPB;  // scale buffers in units of a stage
+  const int NST = p.stages, KPB = p.kpb;
   const uint32_t b_bytes = (uint32_t)p.tn * 64;                     // this CTA's half of B, one K block
   const uint32_t a_stage = 16384u * KPB, stage_bytes = a_stage + b_bytes * KPB;
-  // E4M3 operands, E8M0 scales (byte 0 of a word), fp32 sums
+  // E4M3 operands, E8M0 scales, fp32 sums; the scales' byte (bits 4 and 29) is set per K block
   const uint32_t IDESC = (1u << 23) | ((uint32_t)p.tn >> 3 << 17) | (256u >> 4 << 24);
 
   const uint32_t raw = smem_u32(smem_raw);
   unsigned char *base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   unsigned char *stg_all = base + (size_t)NST * stage_bytes;
   uint64_t *bars = (uint64_t *)(stg_all + F8G_STG);
-  uint32_t *tmem_slot = (uint32_t *)(bars + 2 * NST + 5);
+  uint32_t *tmem_slot = (uint32_t *)(bars + 2 * NST + 5 + 2 * F8G_SF_BUFS);
   volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
   int *prefix = (int *)(stg_all + F8G_STG + 256);
   int *start = prefix + p.E + 1;
@@ -189,16 +192,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
   auto empty_bar = [&](int s) { return smem_u32(bars + NST + s); };
   auto accf_bar = [&](int b) { return smem_u32(bars + 2 * NST + b); };
   auto acce_bar = [&](int b) { return smem_u32(bars + 2 * NST + 2 + b); };
-  const uint32_t drain_bar = smem_u32(bars + 2 * NST + 4);
+  auto sff_bar = [&](int u) { return smem_u32(bars + 2 * NST + 4 + u); };
+  auto sfe_bar = [&](int u) { return smem_u32(bars + 2 * NST + 4 + F8G_SF_BUFS + u); };
+  const uint32_t drain_bar = smem_u32(bars + 2 * NST + 4 + 2 * F8G_SF_BUFS);
 
   if (tid == 0) {
     for (int s = 0; s < NST; ++s) {
-      mbar_init(full_bar(s), 1 + 2 * 4);  // the operands' bytes, and the scale warps of both CTAs
+      mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);
       mbar_init(acce_bar(b), 2 * F8G_STORE_WARPS);
+    }
+    for (int u = 0; u < F8G_SF_BUFS; ++u) {
+      mbar_init(sff_bar(u), 2 * 4);  // the scale warps of both CTAs
+      mbar_init(sfe_bar(u), 1);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -227,9 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
 
   if (warp < 4) {
     // ------------------------------------------------------------ scales (both CTAs)
-    // Unit i (the i-th stage's K blocks) uses scale buffers (i % SFU) KPB ..; its predecessor there,
-    // unit i - SFU, is done when the stage it used is released. That stage (NST >= SFU stages
-    // in turn) cannot be released again before unit i is written, so the parity is unambiguous.
+    // Unit: up to four K blocks of a tile, read one unit ahead of the buffer's release.
     const int nkb = (p.K + QB - 1) / QB, nnb = (p.N + QB - 1) / QB, nw = (p.tn + 31) / 32;
     int tile = pair, kb = 0;
     F8Tile t;
@@ -249,63 +256,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
         pa[i] = WGRAD ? p.a_scale + (size_t)t.kofs * p.M + r : p.a_scale + (size_t)(t.row0 + r) * nkb;
       }
     };
-    uint32_t wa[2][4], wb[2][8];  // bytes of the next unit
+    // the next unit's bytes of 4 rows of A and up to 8 of B (one word each where the bytes of four
+    // K blocks are one aligned word); columns past N and K blocks past the last read as 0
+    uint32_t w[12][F8G_SF_K];
+    const bool va = !WGRAD && nkb % 4 == 0 && ((uintptr_t)p.a_scale & 3u) == 0;
+    const bool vb = !WGRAD && nkb % 4 == 0 && ((uintptr_t)p.b_scale & 3u) == 0;
     auto fetch = [&]() {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int k = kb + j;
-        const bool on = j < KPB && k < t.nk;
+      for (int i = 0; i < 12; ++i) {
+        const int c = t.n0 + 32 * (i - 4) + lane;
+        const bool on = i < 4 ? oa[i < 4 ? i : 0] : i - 4 < nw && c < p.N;
+        const uint8_t *src = i < 4 ? pa[i < 4 ? i : 0]
+                             : WGRAD ? p.b_scale + (size_t)t.kofs * p.N + c
+                                     : p.b_scale + ((size_t)t.g * nnb + c / QB) * nkb;
+        const size_t step = WGRAD ? (size_t)(i < 4 ? p.M : p.N) : 1;
+        const bool word = i < 4 ? va : vb;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          wa[j][i] = on && oa[i] ? __ldg(pa[i] + (WGRAD ? (size_t)k * p.M : (size_t)k)) : 0u;
+        for (int j = 0; j < F8G_SF_K; ++j) w[i][j] = 0u;
+        if (on && word) w[i][0] = __ldg((const uint32_t *)(src + kb));
+        if (on && !word)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = t.n0 + 32 * i + lane;
-          wb[j][i] = !(on && i < nw && c < p.N) ? 0u
-                     : WGRAD ? __ldg(p.b_scale + (size_t)(t.kofs + k) * p.N + c)
-                             : __ldg(p.b_scale + ((size_t)t.g * nnb + c / QB) * nkb + k);
-        }
+          for (int j = 0; j < F8G_SF_K; ++j)
+            if (kb + j < t.nk) w[i][j] = __ldg(src + (size_t)(kb + j) * step);
       }
     };
     enter();
     if (tile < total) fetch();
     const uint32_t quarter = (uint32_t)(warp * 32) << 16;
-    int unit = 0, mine = 0, stage = 0;  // i % SFU; i's stage; the stage that unit i - SFU used
+    int unit = 0;
     uint32_t phase = 0;
-    for (int i = 0; tile < total; ++i) {
-      uint32_t va[2][4], vb[2][8];
+    while (tile < total) {
+      uint32_t v[12];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) va[j][x] = wa[j][x] * 0x01010101u;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) vb[j][x] = wb[j][x] * 0x01010101u;
-      }
-      const int used = min(KPB, t.nk - kb);
-      kb += KPB;
+      for (int i = 0; i < 12; ++i) v[i] = w[i][0] | w[i][1] << 8 | w[i][2] << 16 | w[i][3] << 24;
+      kb += F8G_SF_K;
       if (kb >= t.nk) {
         tile += npairs;
         enter();
       }
       if (tile < total) fetch();
-      if (i >= SFU) {
-        if (!f8_wait_warp(empty_bar(stage), phase, abort_flag, limit, INFO_WAIT_MMA_EMPTY)) break;
-        if (++stage == NST) { stage = 0; phase ^= 1u; }
-        tc_fence_after();
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (j < used) {
-          const uint32_t at = sf_col(unit * KPB + j) + quarter;
-          tmem_st4(at, va[j]);
-          tmem_st8(at + 4, vb[j]);
-        }
+      if (!f8_wait_warp(sfe_bar(unit), phase ^ 1u, abort_flag, limit, INFO_WAIT_MMA_EMPTY)) break;
+      tc_fence_after();
+      tmem_st4(sf_col(unit) + quarter, v);
+      tmem_st8(sf_col(unit) + 4 + quarter, v + 4);
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cta0(full_bar(mine));
-      if (++mine == NST) mine = 0;
-      if (++unit == SFU) unit = 0;
+      if (lane == 0) mbar_arrive_cta0(sff_bar(unit));
+      if (++unit == F8G_SF_BUFS) { unit = 0; phase ^= 1u; }
     }
   } else if (warp == 12) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
@@ -357,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
       // the tensor core drains its queue in a few hundred cycles: between two stages this thread does
       // one inlined barrier test, and the descriptors are kept as running values
       int stage = 0, acc = 0, unit = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      uint32_t phase = 0, acc_phase = 0, unit_phase = 0;
       bool ok = true, any = false;
       const uint64_t adesc0 = make_sdesc(smem_u32(base)), bdesc0 = make_sdesc(smem_u32(base) + a_stage);
       int nk = pair < total ? f8_blocks<WGRAD>(p, pair, prefix, start) : 0;
@@ -372,30 +370,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
         }
         const uint32_t d = tmem_base + (uint32_t)(acc * 256);
         uint32_t accumulate = 0;
-        for (int left = left0; left > 0; left -= KPB) {
-          if (!mbar_try_wait(full_bar(stage), phase) &&
-              !mbar_wait(full_bar(stage), phase, abort_flag, limit, INFO_WAIT_TMA_FULL)) {
+        for (int kb = 0; kb < left0; kb += KPB) {
+          const bool first = kb % F8G_SF_K == 0;  // of a scale unit
+          if ((first && !mbar_try_wait(sff_bar(unit), unit_phase) &&
+               !mbar_wait(sff_bar(unit), unit_phase, abort_flag, limit, INFO_WAIT_TMA_FULL)) ||
+              (!mbar_try_wait(full_bar(stage), phase) &&
+               !mbar_wait(full_bar(stage), phase, abort_flag, limit, INFO_WAIT_TMA_FULL))) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint64_t off = (uint64_t)(((uint32_t)stage * stage_bytes) >> 4);
           uint64_t ad = adesc0 + off, bd = bdesc0 + off;
-          uint32_t sf = sf_col(unit * KPB);
-          for (int j = 0; j < min(KPB, left); ++j) {
+          const uint32_t sf = sf_col(unit);
+          for (int j = 0; j < min(KPB, left0 - kb); ++j) {
+            const uint32_t byte = (uint32_t)(kb + j) % F8G_SF_K;
+            const uint32_t idesc = IDESC | byte << 4 | byte << 29;
 #pragma unroll
             for (int k32 = 0; k32 < 4; ++k32) {  // 32 bytes of K: two 16-byte units further
-              f8_mma(d, ad + 2 * k32, bd + 2 * k32, IDESC, sf, sf + 4, accumulate);
+              f8_mma(d, ad + 2 * k32, bd + 2 * k32, idesc, sf, sf + 4, accumulate);
               accumulate = 1;
             }
             ad += 16384 >> 4;
             bd += b_bytes >> 4;
-            sf += 16;  // the two K blocks of a stage use neighbouring scale buffers
           }
           any = true;
           tc2_commit_both(empty_bar(stage));
           if (++stage == NST) { stage = 0; phase ^= 1u; }
-          if (++unit == SFU) unit = 0;
+          if ((kb + KPB) % F8G_SF_K == 0 || kb + KPB >= left0) {
+            tc2_commit_both(sfe_bar(unit));
+            if (++unit == F8G_SF_BUFS) { unit = 0; unit_phase ^= 1u; }
+          }
         }
         if (!ok) break;
         tc2_commit_both(accf_bar(acc));
