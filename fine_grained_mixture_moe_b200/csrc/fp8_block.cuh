@@ -75,7 +75,21 @@ template <int V> struct Pack<float, V> {
       v[4 * i + 3] = r[i].w;
     }
   }
+  __device__ __forceinline__ void values4(int j, float (&v)[4]) const {  // elements 4 j .. 4 j + 3
+    v[0] = r[j].x;
+    v[1] = r[j].y;
+    v[2] = r[j].z;
+    v[3] = r[j].w;
+  }
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i)
+      m = max(m, max(max(abs_bits(r[i].x), abs_bits(r[i].y)), max(abs_bits(r[i].z), abs_bits(r[i].w))));
+    return m;
+  }
 };
+// (amax: the bits of the largest magnitude)
 template <int V> struct Pack<__nv_bfloat16, V> {
   static_assert(V % 8 == 0, "16-byte loads");
   uint4 r[V / 8];
@@ -98,6 +112,23 @@ template <int V> struct Pack<__nv_bfloat16, V> {
       }
     }
   }
+  __device__ __forceinline__ void values4(int j, float (&v)[4]) const {
+    const uint32_t a = j & 1 ? r[j / 2].z : r[j / 2].x, b = j & 1 ? r[j / 2].w : r[j / 2].y;
+    v[0] = __uint_as_float(a << 16);
+    v[1] = __uint_as_float(a & 0xffff0000u);
+    v[2] = __uint_as_float(b << 16);
+    v[3] = __uint_as_float(b & 0xffff0000u);
+  }
+  __device__ __forceinline__ uint32_t amax() const {  // two at a time: magnitudes order as integers
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < V / 8; ++i) {
+      const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = __vmaxu2(m, w[j] & 0x7fff7fffu);
+    }
+    return max(m << 16, m & 0x7fff0000u);
+  }
 };
 // E4M3 codes (a row's block scale applied by the caller).
 template <int V> struct Pack<uint8_t, V> {
@@ -105,16 +136,13 @@ template <int V> struct Pack<uint8_t, V> {
   uint4 r;
   __device__ __forceinline__ void load(const uint8_t *p) { r = __ldg((const uint4 *)p); }
   __device__ __forceinline__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void values(float (&v)[V]) const {
+  __device__ __forceinline__ void values4(int j, float (&v)[4]) const {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 a = e4m3x2_values(w[j] & 0xffffu), b = e4m3x2_values(w[j] >> 16);
-      v[4 * j] = a.x;
-      v[4 * j + 1] = a.y;
-      v[4 * j + 2] = b.x;
-      v[4 * j + 3] = b.y;
-    }
+    const float2 a = e4m3x2_values(w[j] & 0xffffu), b = e4m3x2_values(w[j] >> 16);
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = b.x;
+    v[3] = b.y;
   }
 };
 
@@ -150,57 +178,87 @@ __device__ __forceinline__ long long valid_rows(long long rows, const int32_t *n
   return n_rows ? min(rows, (long long)max(__ldg(n_rows), 0)) : rows;
 }
 
-// A thread's walk over the (row, block) pairs of a [rows, nblk] grid of blocks in steps of
-// `step` blocks: one division at the start, none per step.
-struct BlockWalk {
-  long long row, drow;
-  int blk, dblk, nblk;
-  __device__ __forceinline__ BlockWalk(long long first, long long step, int nb) : nblk(nb) {
-    row = first / nb;
-    blk = (int)(first - row * nb);
-    drow = step / nb;
-    dblk = (int)(step - drow * nb);
-  }
-  __device__ __forceinline__ void next() {
-    row += drow;
-    blk += dblk;
-    if (blk >= nblk) {
-      blk -= nblk;
-      ++row;
-    }
-  }
+// Row-wise kernels: a team of 8 lanes per block of 128, 16 values per lane (8 at 8 l and 8 at
+// 64 + 8 l, so that each 16-byte load of bf16 and 8-byte store of codes is contiguous over the team).
+// With 8 values per lane the kernels issued twice the instructions per value and were bound by
+// that. Teams take every `step`-th block of the flat list; a warp's four teams walk together (the
+// shuffles need every lane), lanes past the end work on zeros.
+constexpr int RT_LANES = 8, RT_TEAMS = 256 / RT_LANES;
+struct RowTeam {
+  long long first;  // this warp's first block
+  long long step;
+  int team, c;      // team in the warp, first column of this lane
+  __device__ __forceinline__ RowTeam()
+      : first((long long)blockIdx.x * RT_TEAMS + (threadIdx.x >> 5) * 4), step((long long)gridDim.x * RT_TEAMS),
+        team((threadIdx.x & 31) / RT_LANES), c((threadIdx.x % RT_LANES) * 8) {}
 };
+// 16 values of a block at src + c and src + c + 64.
+template <typename T> struct Lane16 {
+  Pack<T, 8> p[2];
+  __device__ __forceinline__ void load(const T *src) {
+    p[0].load(src);
+    p[1].load(src + 64);
+  }
+  __device__ __forceinline__ void zero() {
+    p[0].zero();
+    p[1].zero();
+  }
+  __device__ __forceinline__ uint32_t amax() const { return max(p[0].amax(), p[1].amax()); }
+};
+__device__ __forceinline__ uint32_t block_byte(uint32_t lane_amax) {
+  return e8m0_of_amax(team_max<RT_LANES>(lane_amax));
+}
 
 // ------------------------------------------------------------------ rows, 1 x 128 blocks
-// A team of 128 / V lanes per block (V elements in one 16-byte load per lane), so a warp's loads
-// and stores are contiguous.
-template <typename Tin>
-__global__ void __launch_bounds__(256)
+constexpr int F8Q_U = 2;  // blocks in flight per team: 64 bytes per lane, which HBM's latency asks for
+
+// FULL: cols a multiple of 128, so a block's flat number places it without its row and column.
+template <typename Tin, bool FULL>
+__global__ void __launch_bounds__(256, 4)
     quantize_block_rows_kernel(const Tin *__restrict__ in, long long rows, int cols, int nblk,
                                const int32_t *__restrict__ n_rows, uint8_t *__restrict__ q,
                                uint8_t *__restrict__ scale) {
-  constexpr int V = 16 / sizeof(Tin), L = QB / V, TPB = 256 / L;
+  constexpr int U = F8Q_U;
   const KernelStamp stamp(K_F8B_QUANT);
   griddep_wait();
   stamp.started();
   griddep_launch();
-  const long long nr = valid_rows(rows, n_rows);
-  const int c0 = (threadIdx.x % L) * V;
-  BlockWalk w((long long)blockIdx.x * TPB + threadIdx.x / L, (long long)gridDim.x * TPB, nblk);
-  // whole warps walk together (the shuffles need every lane): a lane past the end works on zeros
-  const long long total = nr * nblk;
-  for (long long b0 = (long long)blockIdx.x * TPB + (threadIdx.x / 32) * (32 / L); b0 < total;
-       b0 += (long long)gridDim.x * TPB, w.next()) {
-    const int col = w.blk * QB + c0;
-    const bool ok = w.row < nr && col < cols;
-    Pack<Tin, V> p;
-    if (ok) p.load(in + w.row * cols + col);
-    else p.zero();
-    float v[V];
-    p.values(v);
-    const uint32_t b = e8m0_of_amax(team_max<L>(amax_bits(v)));
-    if (ok) store_codes(q + w.row * cols + col, v, e8m0_inverse(b));
-    if (c0 == 0 && w.row < nr) scale[w.row * nblk + w.blk] = (uint8_t)b;
+  const RowTeam w;
+  const long long total = valid_rows(rows, n_rows) * nblk;
+  for (long long b0 = w.first; b0 < total; b0 += U * w.step) {
+    Lane16<Tin> x[U];
+    long long off[U];
+    bool ok[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long b = b0 + u * w.step + w.team;
+      ok[u][0] = ok[u][1] = b < total;
+      if (FULL) {
+        off[u] = b * QB + w.c;
+      } else {
+        const long long row = b / nblk;
+        const int col = (int)(b - row * nblk) * QB + w.c;
+        off[u] = row * cols + col;
+        ok[u][0] &= col < cols;
+        ok[u][1] &= col + 64 < cols;
+      }
+      x[u].zero();
+      if (ok[u][0]) x[u].p[0].load(in + off[u]);
+      if (ok[u][1]) x[u].p[1].load(in + off[u] + 64);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long b = b0 + u * w.step + w.team;
+      const uint32_t byte = block_byte(x[u].amax());
+      const float inv = e8m0_inverse(byte);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[8];
+        x[u].p[h].values(v);
+        if (ok[u][h]) store_codes(q + off[u] + 64 * h, v, inv);
+      }
+      if (w.c == 0 && b < total) scale[b] = (uint8_t)byte;
+    }
   }
 }
 
@@ -235,26 +293,33 @@ __device__ __forceinline__ void tile_put(uint32_t *tile, int a, int col, const u
     }
   }
 }
-// Columns of the tile to dst[c * pitch + r], c < cols, r < rows (a multiple of 4): one warp per
-// column, 4 rows per lane.
+// Columns of the tile to dst[c * pitch + r], c < cols, r < rows (a multiple of 16): 8 lanes per column,
+// 16 rows per lane. The key permutes the words of a 16-byte group among themselves and the groups of
+// a column among themselves.
 template <int V>
 __device__ __forceinline__ void tile_write(const uint32_t *tile, uint8_t *dst, size_t pitch, int cols,
                                            int rows) {
-  const int lane = threadIdx.x & 31;
-  for (int c = threadIdx.x >> 5; c < cols; c += F8T_THREADS / 32)
-    if (4 * lane < rows) *(uint32_t *)(dst + c * pitch + 4 * lane) = tile[c * 32 + (lane ^ tile_key<V>(c))];
+  const int g = threadIdx.x & 7;
+  for (int c = threadIdx.x >> 3; c < cols; c += F8T_THREADS / 8) {
+    if (16 * g >= rows) continue;
+    const int key = tile_key<V>(c);
+    uint4 v = *(const uint4 *)(tile + c * 32 + 4 * (g ^ (key >> 2)));
+    if (key & 1) v = make_uint4(v.y, v.x, v.w, v.z);
+    if (key & 2) v = make_uint4(v.z, v.w, v.x, v.y);
+    *(uint4 *)(dst + c * pitch + 16 * g) = v;
+  }
 }
 
 // ------------------------------------------------------------------ weights, 128 x 128 blocks
 // One CTA per block; q_t, scale_t (may be null) receive the transposed matrix, whose blocks and
 // scales are the same ones.
 template <typename Tin>
-__global__ void __launch_bounds__(F8T_THREADS)
+__global__ void __launch_bounds__(F8T_THREADS, sizeof(Tin) == 4 ? 2 : 4)
     quantize_block_weight_kernel(const Tin *__restrict__ in, int rows, int cols,
                                  uint8_t *__restrict__ q, uint8_t *__restrict__ scale,
                                  uint8_t *__restrict__ q_t, uint8_t *__restrict__ scale_t) {
   constexpr int V = 16 / sizeof(Tin), L = QB / V, A = F8T_THREADS / L, PASS = 32 / A;
-  __shared__ uint32_t tile[QB * 32];
+  __shared__ __align__(16) uint32_t tile[QB * 32];
   __shared__ uint32_t wmax[F8T_THREADS / 32];
   const KernelStamp stamp(K_F8B_QUANT);
   griddep_wait();
@@ -277,11 +342,7 @@ __global__ void __launch_bounds__(F8T_THREADS)
 #pragma unroll
   for (int s = 0; s < PASS; ++s)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v[V];
-      p[s][i].values(v);
-      m = max(m, amax_bits(v));
-    }
+    for (int i = 0; i < 4; ++i) m = max(m, p[s][i].amax());
   m = team_max<32>(m);
   if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
   __syncthreads();
@@ -360,14 +421,14 @@ __device__ __forceinline__ bool find_token_block(const int32_t *offsets, int E, 
 // to scale_t [., cols]. Rows past the expert's last are zeros. Tin uint8_t: E4M3 codes with 1 x 128
 // scale bytes in_scale [rows, ceil(cols / 128)] (an 8-bit checkpoint), read without a bf16 copy.
 template <typename Tin>
-__global__ void __launch_bounds__(F8T_THREADS)
+__global__ void __launch_bounds__(F8T_THREADS, sizeof(Tin) == 4 ? 2 : 4)
     quantize_block_tokens_kernel(const Tin *__restrict__ in, const uint8_t *__restrict__ in_scale,
                                  long long rows, int cols, const int32_t *__restrict__ offsets, int E,
                                  uint8_t *__restrict__ q_t, size_t pitch,
                                  uint8_t *__restrict__ scale_t) {
   constexpr int V = 16 / sizeof(Tin), L = QB / V, A = F8T_THREADS / L, PASS = 32 / A;
-  __shared__ uint32_t tile[QB * 32];
-  __shared__ uint32_t cmax[F8T_THREADS / 32][QB];
+  __shared__ __align__(16) uint32_t tile[QB * 32];
+  __shared__ __align__(16) uint32_t cmax[F8T_THREADS / 32][QB];
   const KernelStamp stamp(K_F8B_QUANT);
   griddep_wait();
   stamp.started();
@@ -394,25 +455,27 @@ __global__ void __launch_bounds__(F8T_THREADS)
         p[s][i].zero();
       }
     }
-  uint32_t m[V];
+  // column maxima, four columns (one word of codes to come) at a time
 #pragma unroll
-  for (int j = 0; j < V; ++j) m[j] = 0;
+  for (int j = 0; j < V / 4; ++j) {
+    uint32_t m[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int s = 0; s < PASS; ++s)
+    for (int s = 0; s < PASS; ++s)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v[V];
-      p[s][i].values(v);
+      for (int i = 0; i < 4; ++i) {
+        float v[4];
+        p[s][i].values4(j, v);
 #pragma unroll
-      for (int j = 0; j < V; ++j) m[j] = max(m[j], abs_bits(v[j] * rs[s][i]));
+        for (int x = 0; x < 4; ++x) m[x] = max(m[x], abs_bits(v[x] * rs[s][i]));
+      }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+#pragma unroll
+      for (int o = L; o < 32; o <<= 1)  // lanes of the warp that hold the same columns
+        m[x] = max(m[x], __shfl_xor_sync(0xffffffffu, m[x], o));
     }
-#pragma unroll
-  for (int o = L; o < 32; o <<= 1)  // lanes of the warp that hold the same columns
-#pragma unroll
-    for (int j = 0; j < V; ++j) m[j] = max(m[j], __shfl_xor_sync(0xffffffffu, m[j], o));
-  if (lane < L)
-#pragma unroll
-    for (int j = 0; j < V; ++j) cmax[warp][c0 + j] = m[j];
+    if (lane < L) *(uint4 *)&cmax[warp][c0 + 4 * j] = make_uint4(m[0], m[1], m[2], m[3]);
+  }
   __syncthreads();
   if (threadIdx.x < QB) {
     uint32_t x = 0;
@@ -424,22 +487,19 @@ __global__ void __launch_bounds__(F8T_THREADS)
     cmax[0][threadIdx.x] = __float_as_uint(e8m0_inverse(b));
   }
   __syncthreads();
-  float inv[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) inv[j] = __uint_as_float(cmax[0][c0 + j]);
 #pragma unroll
   for (int s = 0; s < PASS; ++s) {
     uint32_t w[4][V / 4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v[V];
-      p[s][i].values(v);
+    for (int j = 0; j < V / 4; ++j) {
+      const float4 inv = *(const float4 *)&cmax[0][c0 + 4 * j];
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[j] *= rs[s][i];
-#pragma unroll
-      for (int j = 0; j < V / 4; ++j)
-        w[i][j] = e4m3x4(v[4 * j] * inv[4 * j], v[4 * j + 1] * inv[4 * j + 1],
-                         v[4 * j + 2] * inv[4 * j + 2], v[4 * j + 3] * inv[4 * j + 3]);
+      for (int i = 0; i < 4; ++i) {
+        float v[4];
+        p[s][i].values4(j, v);
+        w[i][j] = e4m3x4(v[0] * rs[s][i] * inv.x, v[1] * rs[s][i] * inv.y, v[2] * rs[s][i] * inv.z,
+                         v[3] * rs[s][i] * inv.w);
+      }
     }
     tile_put<V>(tile, a0 + s * A, c0, w);
   }
@@ -449,64 +509,97 @@ __global__ void __launch_bounds__(F8T_THREADS)
 }
 
 // ------------------------------------------------------------------ SwiGLU with a checkpoint
-// sigmoid(z) = 1 / (1 + e^-z): for z below about -88 the exponential is infinite and the result 0.
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// sigmoid(z) = 1 / (1 + 2^(-z log2 e)) by the fast exponential and reciprocal (2 ulp and 1 ulp);
+// for z below about -88 the exponential is infinite and the result 0.
+__device__ __forceinline__ float sigmoid_f(float z) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * z));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
+// Walk over the blocks of h [., f] in flat order and the offsets of their gate columns in
+// [., 2 f] rows (the up columns are f further): no division per step.
+struct GateWalk {
+  long long gate;  // offset of this lane's gate columns
+  int blk, nb, dblk;
+  long long dgate;
+  int f;
+  __device__ __forceinline__ GateWalk(const RowTeam &w, int f_) : nb(f_ / QB), f(f_) {
+    const long long b = w.first + w.team, row = b / nb;
+    blk = (int)(b - row * nb);
+    gate = row * 2 * f + blk * QB + w.c;
+    const long long drow = w.step / nb;
+    dblk = (int)(w.step - drow * nb);
+    dgate = drow * 2 * f + dblk * QB;
+  }
+  __device__ __forceinline__ void next() {
+    gate += dgate;
+    blk += dblk;
+    if (blk >= nb) {  // the next row, nb blocks back
+      blk -= nb;
+      gate += f;
+    }
+  }
+};
 
 // gu [rows, 2 f] = [gate | up]: h = silu(g) u, to h (bf16) and / or h_q + h_scale (the down product's
 // operand, quantised from the fp32 value), and the E4M3 codes of gu itself to gu_q + gu_scale (the
 // checkpoint of the backward pass). f a multiple of 128, so no block spans gate and up.
 template <typename Tin>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
     swiglu_checkpoint_kernel(const Tin *__restrict__ gu, long long rows, int f,
                              const int32_t *__restrict__ n_rows, __nv_bfloat16 *__restrict__ h,
                              uint8_t *__restrict__ h_q, uint8_t *__restrict__ h_scale,
                              uint8_t *__restrict__ gu_q, uint8_t *__restrict__ gu_scale) {
-  constexpr int V = 8, L = QB / V, TPB = 256 / L;
   const KernelStamp stamp(K_F8B_SWIGLU);
   griddep_wait();
   stamp.started();
   griddep_launch();
-  const long long nr = valid_rows(rows, n_rows);
-  const int nb = f / QB, c0 = (threadIdx.x % L) * V;
-  BlockWalk w((long long)blockIdx.x * TPB + threadIdx.x / L, (long long)gridDim.x * TPB, nb);
-  const long long total = nr * nb;
-  for (long long b0 = (long long)blockIdx.x * TPB + (threadIdx.x / 32) * (32 / L); b0 < total;
-       b0 += (long long)gridDim.x * TPB, w.next()) {
-    const int col = w.blk * QB + c0;
-    const bool ok = w.row < nr;
-    Pack<Tin, V> pg, pu;
+  const RowTeam w;
+  GateWalk at(w, f);
+  const long long total = valid_rows(rows, n_rows) * at.nb;
+  for (long long b0 = w.first; b0 < total; b0 += w.step, at.next()) {
+    const long long b = b0 + w.team, off = b * QB + w.c;  // in h
+    const bool ok = b < total;
+    Lane16<Tin> xg, xu;
+    xg.zero();
+    xu.zero();
     if (ok) {
-      pg.load(gu + w.row * 2 * f + col);
-      pu.load(gu + w.row * 2 * f + f + col);
-    } else {
-      pg.zero();
-      pu.zero();
+      xg.load(gu + at.gate);
+      xu.load(gu + at.gate + f);
     }
-    float g[V], u[V], hv[V];
-    pg.values(g);
-    pu.values(u);
-#pragma unroll
-    for (int i = 0; i < V; ++i) hv[i] = g[i] * sigmoid_f(g[i]) * u[i];
+    uint32_t bg = 0, bu = 0;
     if (gu_q) {
-      const uint32_t bg = e8m0_of_amax(team_max<L>(amax_bits(g)));
-      const uint32_t bu = e8m0_of_amax(team_max<L>(amax_bits(u)));
-      if (ok) {
-        store_codes(gu_q + w.row * 2 * f + col, g, e8m0_inverse(bg));
-        store_codes(gu_q + w.row * 2 * f + f + col, u, e8m0_inverse(bu));
-        if (c0 == 0) {
-          gu_scale[w.row * 2 * nb + w.blk] = (uint8_t)bg;
-          gu_scale[w.row * 2 * nb + nb + w.blk] = (uint8_t)bu;
-        }
+      bg = block_byte(xg.amax());
+      bu = block_byte(xu.amax());
+      // the gate block's scale sits where the block does, in rows of 2 nb
+      if (ok && w.c == 0) {
+        gu_scale[at.gate / QB] = (uint8_t)bg;
+        gu_scale[at.gate / QB + at.nb] = (uint8_t)bu;
       }
+    }
+    float hv[2][8];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float g[8], u[8];
+      xg.p[x].values(g);
+      xu.p[x].values(u);
+      if (gu_q && ok) {
+        store_codes(gu_q + at.gate + 64 * x, g, e8m0_inverse(bg));
+        store_codes(gu_q + at.gate + f + 64 * x, u, e8m0_inverse(bu));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hv[x][i] = g[i] * sigmoid_f(g[i]) * u[i];
+      if (h && ok) store_bf16x8(h + off + 64 * x, hv[x]);
     }
     if (h_q) {
-      const uint32_t bh = e8m0_of_amax(team_max<L>(amax_bits(hv)));
+      const uint32_t bh = block_byte(max(amax_bits(hv[0]), amax_bits(hv[1])));
       if (ok) {
-        store_codes(h_q + w.row * f + col, hv, e8m0_inverse(bh));
-        if (c0 == 0) h_scale[w.row * nb + w.blk] = (uint8_t)bh;
+        store_codes(h_q + off, hv[0], e8m0_inverse(bh));
+        store_codes(h_q + off + 64, hv[1], e8m0_inverse(bh));
+        if (w.c == 0) h_scale[b] = (uint8_t)bh;
       }
     }
-    if (h && ok) store_bf16x8(h + w.row * f + col, hv);
   }
 }
 
@@ -514,72 +607,81 @@ __global__ void __launch_bounds__(256)
 // dgu = [dg | du] in bf16 and / or as E4M3 codes (the input gradient's operand, quantised from the
 // fp32 values); h in bf16 (the down weight gradient's operand).
 template <typename Tin>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
     swiglu_checkpoint_backward_kernel(const uint8_t *__restrict__ gu_q,
                                       const uint8_t *__restrict__ gu_scale,
                                       const Tin *__restrict__ dh, long long rows, int f,
                                       const int32_t *__restrict__ n_rows,
                                       __nv_bfloat16 *__restrict__ dgu, uint8_t *__restrict__ dgu_q,
                                       uint8_t *__restrict__ dgu_scale, __nv_bfloat16 *__restrict__ h) {
-  constexpr int V = 8, L = QB / V, TPB = 256 / L;
   const KernelStamp stamp(K_F8B_SWIGLU);
   griddep_wait();
   stamp.started();
   griddep_launch();
-  const long long nr = valid_rows(rows, n_rows);
-  const int nb = f / QB, c0 = (threadIdx.x % L) * V;
-  BlockWalk w((long long)blockIdx.x * TPB + threadIdx.x / L, (long long)gridDim.x * TPB, nb);
-  const long long total = nr * nb;
-  for (long long b0 = (long long)blockIdx.x * TPB + (threadIdx.x / 32) * (32 / L); b0 < total;
-       b0 += (long long)gridDim.x * TPB, w.next()) {
-    const int col = w.blk * QB + c0;
-    const bool ok = w.row < nr;
-    const long long at = w.row * 2 * f + col;
-    uint2 cg = make_uint2(0u, 0u), cu = cg;
-    float sg = 1.0f, su = 1.0f;
-    Pack<Tin, V> pd;
+  const RowTeam w;
+  GateWalk at(w, f);
+  const long long total = valid_rows(rows, n_rows) * at.nb;
+  for (long long b0 = w.first; b0 < total; b0 += w.step, at.next()) {
+    const long long b = b0 + w.team, off = b * QB + w.c;
+    const bool ok = b < total;
+    uint2 cg[2], cu[2];
+    uint32_t sg = 127, su = 127;
+    Lane16<Tin> xd;
+    xd.zero();
+    cg[0] = cg[1] = cu[0] = cu[1] = make_uint2(0u, 0u);
     if (ok) {
-      cg = __ldg((const uint2 *)(gu_q + at));
-      cu = __ldg((const uint2 *)(gu_q + at + f));
-      sg = e8m0_value(__ldg(gu_scale + w.row * 2 * nb + w.blk));
-      su = e8m0_value(__ldg(gu_scale + w.row * 2 * nb + nb + w.blk));
-      pd.load(dh + w.row * f + col);
-    } else {
-      pd.zero();
-    }
-    float d[V], dg[V], du[V], hv[V];
-    pd.values(d);
-    const uint32_t wg[2] = {cg.x, cg.y}, wu[2] = {cu.x, cu.y};
 #pragma unroll
-    for (int i = 0; i < V; i += 2) {
-      const float2 g2 = e4m3x2_values((wg[i / 4] >> (8 * (i % 4))) & 0xffffu);
-      const float2 u2 = e4m3x2_values((wu[i / 4] >> (8 * (i % 4))) & 0xffffu);
-      const float gg[2] = {g2.x * sg, g2.y * sg}, uu[2] = {u2.x * su, u2.y * su};
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float s = sigmoid_f(gg[j]), gs = gg[j] * s;
-        du[i + j] = d[i + j] * gs;
-        dg[i + j] = d[i + j] * uu[j] * (s * (1.0f + gg[j] * (1.0f - s)));
-        hv[i + j] = gs * uu[j];
+      for (int x = 0; x < 2; ++x) {
+        cg[x] = __ldg((const uint2 *)(gu_q + at.gate + 64 * x));
+        cu[x] = __ldg((const uint2 *)(gu_q + at.gate + f + 64 * x));
       }
+      xd.load(dh + off);
+      sg = __ldg(gu_scale + at.gate / QB);
+      su = __ldg(gu_scale + at.gate / QB + at.nb);
+    }
+    const float vg = e8m0_value(sg), vu = e8m0_value(su);
+    float dg[2][8], du[2][8];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float d[8], hv[8];
+      xd.p[x].values(d);
+      const uint32_t wg[2] = {cg[x].x, cg[x].y}, wu[2] = {cu[x].x, cu[x].y};
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float2 g2 = e4m3x2_values((wg[i / 4] >> (8 * (i % 4))) & 0xffffu);
+        const float2 u2 = e4m3x2_values((wu[i / 4] >> (8 * (i % 4))) & 0xffffu);
+        const float gg[2] = {g2.x * vg, g2.y * vg}, uu[2] = {u2.x * vu, u2.y * vu};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float s = sigmoid_f(gg[j]), gs = gg[j] * s;
+          du[x][i + j] = d[i + j] * gs;
+          // s (1 + g (1 - s)) = s + g s (1 - s)
+          dg[x][i + j] = d[i + j] * uu[j] * fmaf(gs, 1.0f - s, s);
+          hv[i + j] = gs * uu[j];
+        }
+      }
+      if (ok && dgu) {
+        store_bf16x8(dgu + at.gate + 64 * x, dg[x]);
+        store_bf16x8(dgu + at.gate + f + 64 * x, du[x]);
+      }
+      if (ok && h) store_bf16x8(h + off + 64 * x, hv);
     }
     if (dgu_q) {
-      const uint32_t bg = e8m0_of_amax(team_max<L>(amax_bits(dg)));
-      const uint32_t bu = e8m0_of_amax(team_max<L>(amax_bits(du)));
+      const uint32_t bg = block_byte(max(amax_bits(dg[0]), amax_bits(dg[1])));
+      const uint32_t bu = block_byte(max(amax_bits(du[0]), amax_bits(du[1])));
       if (ok) {
-        store_codes(dgu_q + at, dg, e8m0_inverse(bg));
-        store_codes(dgu_q + at + f, du, e8m0_inverse(bu));
-        if (c0 == 0) {
-          dgu_scale[w.row * 2 * nb + w.blk] = (uint8_t)bg;
-          dgu_scale[w.row * 2 * nb + nb + w.blk] = (uint8_t)bu;
+        const float ig = e8m0_inverse(bg), iu = e8m0_inverse(bu);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          store_codes(dgu_q + at.gate + 64 * x, dg[x], ig);
+          store_codes(dgu_q + at.gate + f + 64 * x, du[x], iu);
+        }
+        if (w.c == 0) {
+          dgu_scale[at.gate / QB] = (uint8_t)bg;
+          dgu_scale[at.gate / QB + at.nb] = (uint8_t)bu;
         }
       }
     }
-    if (ok && dgu) {
-      store_bf16x8(dgu + at, dg);
-      store_bf16x8(dgu + at + f, du);
-    }
-    if (ok && h) store_bf16x8(h + w.row * f + col, hv);
   }
 }
 

@@ -143,7 +143,7 @@ moe_status_t moe_swiglu_fp8_forward(const void *gu, int32_t in_dtype, int64_t ro
   MOE_REQUIRE(aligned16(gu) && (!h || aligned16(h)) && (!h_q || aligned16(h_q)) &&
               (!gu_q || aligned16(gu_q)) && (!n_rows || aligned4(n_rows)));
   cudaStream_t st = (cudaStream_t)stream;
-  const dim3 grid(fp8_row_grid(rows * (ffn / QB), 16));
+  const dim3 grid(fp8_row_grid(rows * (ffn / QB), RT_TEAMS));
   ProfScope ps(K_F8B_SWIGLU, st);
   if (in_dtype == MOE_DTYPE_BF16)
     return launch_pdl(swiglu_checkpoint_kernel<__nv_bfloat16>, grid, dim3(256), 0, st,
@@ -165,7 +165,7 @@ moe_status_t moe_swiglu_fp8_backward(const uint8_t *gu_q, const uint8_t *gu_scal
   MOE_REQUIRE(aligned16(gu_q) && gu_scale && aligned16(dh) && (!dgu || aligned16(dgu)) &&
               (!dgu_q || aligned16(dgu_q)) && (!h || aligned16(h)) && (!n_rows || aligned4(n_rows)));
   cudaStream_t st = (cudaStream_t)stream;
-  const dim3 grid(fp8_row_grid(rows * (ffn / QB), 16));
+  const dim3 grid(fp8_row_grid(rows * (ffn / QB), RT_TEAMS));
   ProfScope ps(K_F8B_SWIGLU, st);
   if (dh_dtype == MOE_DTYPE_BF16)
     return launch_pdl(swiglu_checkpoint_backward_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, gu_q,
