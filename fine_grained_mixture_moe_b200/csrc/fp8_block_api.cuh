@@ -88,6 +88,10 @@ moe_status_t moe_gemm_fp8_block(const uint8_t *a, const uint8_t *a_scale, int64_
   if (rows == 0) return MOE_OK;
   MOE_REQUIRE(aligned16(a) && a_scale && aligned16(w) && w_scale && aligned32(out) &&
               (!offsets || aligned4(offsets)));
+  if (few_rows(rows, E, n, k)) {
+    const F8Few f = {a, a_scale, w, w_scale, offsets, out, rows, E, n, k, out_dtype == MOE_DTYPE_F32};
+    return launch_gemm_fp8_few(f, (cudaStream_t)stream);
+  }
   F8Gemm p;
   std::memset(&p, 0, sizeof(p));
   p.offsets = offsets;

@@ -90,3 +90,27 @@ moe_status_t launch_gemm_fp8_block(F8Gemm &p, const uint8_t *a, const uint8_t *b
   ProfScope ps(kind, st);
   return launch_pdl(kern, dim3(2 * pairs), dim3(F8G_THREADS), smem, st, p);
 }
+
+// The form for few rows is chosen by its work in (16 weight rows x 16 rows x one K block) units, half a
+// group per expert taken as unfilled, against what the CTA-pair form takes at least (its start-up,
+// and K). Measured on both sides, few / pairs in us, rows on the first experts | spread over all:
+//   24 experts, n 1280, k 1024:  6 rows 4.3 / 10.4 | 4.3 / 10.4;   96: 8.2 / 10.4 | 10.7 / 14.7;
+//                                192: 12.3 / 10.7 | 13.7 / 14.9;   768: 35 / 11.5 | 39 / 15.3
+//   24 experts, n 1024, k 640:   192: 8.8 / 10.4 | 9.8 / 14.5;     384: 14.1 / 10.6 | 15.8 / 15.0
+//   256 experts, n 1024, k 1024: 32: 7.6 / 10.0 | 11.5 / 16.7;     64: 13.3 / 10.4 | 20.1 / 21.3
+//   8 experts, n 512, k 2048:    256: 10.2 / 13.5 | 11.1 / 13.3;   512: 16.6 / 13.7 | 17.8 / 13.5
+//   1 expert, n = k = 4096:      32: 15.9 / 19.7;                  64: 26.2 / 19.8
+bool few_rows(long long rows, int E, int n, int k) {
+  if (rows > 4096) return false;
+  const int nkb = ceil_div(k, QB);
+  const long long groups2 = 2 * rows / F8F_CHUNK + std::min<long long>(E, rows);  // twice the groups
+  return groups2 * (n / F8F_ROWS) * nkb <= 2 * (9000LL + 400LL * nkb);
+}
+
+moe_status_t launch_gemm_fp8_few(const F8Few &p, cudaStream_t st) {
+  // groups of F8F_CHUNK rows: each of the experts that can have rows wastes at most F8F_CHUNK - 1
+  const long long items = p.offsets ? (p.rows + (F8F_CHUNK - 1) * std::min<long long>(p.E, p.rows)) / F8F_CHUNK
+                                    : ceil_div(p.rows, F8F_CHUNK);
+  ProfScope ps(K_F8B_GEMM, st);
+  return launch_pdl(gemm_fp8_few_kernel, dim3(p.n / F8F_ROWS, (unsigned)items), dim3(32 * F8F_WARPS), 0, st, p);
+}

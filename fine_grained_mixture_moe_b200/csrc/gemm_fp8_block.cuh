@@ -494,4 +494,155 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
   }
 }
 
+// ------------------------------------------------------------------ few rows
+// The same product when the experts have few rows (a served token: one row of each of its top-k
+// experts): the weights' bytes are the work, so one CTA takes 16 weight rows of one expert, its 8 warps
+// share K block by block, and the rows are the narrow side of m16n8k32 instructions. A lane reads 16
+// consecutive codes of a weight row and of a token row; which codes an instruction calls k = 0 .. 31 is
+// free as long as both operands agree, so no shuffle or shared memory lies between the load and the
+// tensor core. Each block of 128 is summed from zero and added with its scales; the warps' sums are
+// added in warp order. Grid: 16-row weight tiles x groups of 16 rows of one expert.
+constexpr int F8F_WARPS = 8, F8F_ROWS = 16, F8F_CHUNK = 16;  // tokens per CTA
+
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+      " {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+struct F8Few {
+  const uint8_t *a, *a_scale, *w, *w_scale;
+  const int32_t *offsets;  // null: one expert with all rows
+  void *out;
+  long long rows;
+  int E, n, k, out_f32;
+};
+
+// Work item j: the j-th group of F8F_CHUNK rows, counted through the experts. Every lane of a warp
+// calls; a lane looks at four experts at a time.
+struct FewItem {
+  int e, cnt;
+  long long row;
+};
+__device__ __forceinline__ bool find_few(const F8Few &p, int j, FewItem *it) {
+  if (!p.offsets) {
+    it->e = 0;
+    it->row = (long long)j * F8F_CHUNK;
+    it->cnt = (int)min((long long)F8F_CHUNK, p.rows - it->row);
+    return it->cnt > 0;
+  }
+  const int lane = threadIdx.x & 31;
+  for (int e0 = 0; e0 < p.E; e0 += 128) {
+    int off[5], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) off[i] = (int)expert_bound(p.offsets, min(e0 + 4 * lane + i, p.E), p.rows);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += max((off[i + 1] - off[i] + F8F_CHUNK - 1) / F8F_CHUNK, 0);
+    const int incl = warp_incl_scan(sum);
+    const unsigned past = __ballot_sync(0xffffffffu, incl > j);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      j -= __shfl_sync(0xffffffffu, incl - sum, src);
+#pragma unroll
+      for (int i = 0; i < 5; ++i) off[i] = __shfl_sync(0xffffffffu, off[i], src);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = max((off[i + 1] - off[i] + F8F_CHUNK - 1) / F8F_CHUNK, 0);
+        if (j >= 0 && j < n) {
+          it->e = e0 + 4 * src + i;
+          it->row = off[i] + j * F8F_CHUNK;
+          it->cnt = min(F8F_CHUNK, off[i + 1] - off[i] - j * F8F_CHUNK);
+          return true;
+        }
+        j -= n;
+      }
+    }
+    j -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
+// NT groups of 8 tokens against 16 weight rows.
+template <int NT>
+__device__ __forceinline__ void few_chunk(const F8Few &p, int e, long long row, int cnt, int n0, float *red) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int nkb = (p.k + QB - 1) / QB, nnb = (p.n + QB - 1) / QB;
+  const uint8_t *wrow = p.w + ((size_t)e * p.n + n0 + g) * p.k + 16 * t;
+  const uint8_t *wsc = p.w_scale + ((size_t)e * nnb + n0 / QB) * nkb;
+  float acc[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+  for (int kb = warp; kb < nkb; kb += F8F_WARPS) {
+    uint4 wa[2][2], xb[NT][2];  // [weight row g, g + 8][64-byte half], [token group][half]
+    float sx[NT][2];
+    const float sw = e8m0_value(__ldg(wsc + kb));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k0 = kb * QB + 64 * h;
+      const bool ok = k0 + 16 * t < p.k;
+      wa[0][h] = wa[1][h] = make_uint4(0u, 0u, 0u, 0u);
+      if (ok) {
+        wa[0][h] = __ldg((const uint4 *)(wrow + k0));
+        wa[1][h] = __ldg((const uint4 *)(wrow + (size_t)8 * p.k + k0));
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        xb[i][h] = make_uint4(0u, 0u, 0u, 0u);
+        if (ok && 8 * i + g < cnt)
+          xb[i][h] = __ldg((const uint4 *)(p.a + (size_t)(row + 8 * i + g) * p.k + k0 + 16 * t));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int tok = 8 * i + 2 * t + j;
+        sx[i][j] = tok < cnt ? e8m0_value(__ldg(p.a_scale + (size_t)(row + tok) * nkb + kb)) : 0.0f;
+      }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mma_e4m3(c, wa[0][h].x, wa[1][h].x, wa[0][h].y, wa[1][h].y, xb[i][h].x, xb[i][h].y);
+        mma_e4m3(c, wa[0][h].z, wa[1][h].z, wa[0][h].w, wa[1][h].w, xb[i][h].z, xb[i][h].w);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(c[j], sx[i][j & 1] * sw, acc[i][j]);
+    }
+  }
+  // red[warp][token][16 weight rows]
+  float *mine = red + (size_t)warp * NT * 8 * 16;
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mine[(8 * i + 2 * t + (j & 1)) * 16 + g + 8 * (j >> 1)] = acc[i][j];
+  __syncthreads();
+  for (int o = threadIdx.x; o < min(cnt, NT * 8) * 16; o += 32 * F8F_WARPS) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < F8F_WARPS; ++w) s += red[(size_t)w * NT * 8 * 16 + o];
+    const size_t at = (size_t)(row + o / 16) * p.n + n0 + o % 16;
+    if (p.out_f32) ((float *)p.out)[at] = s;
+    else ((__nv_bfloat16 *)p.out)[at] = __float2bfloat16_rn(s);
+  }
+}
+
+__global__ void __launch_bounds__(32 * F8F_WARPS, 4) gemm_fp8_few_kernel(const __grid_constant__ F8Few p) {
+  __shared__ float red[F8F_WARPS * F8F_CHUNK * 16];
+  const KernelStamp stamp(K_F8B_GEMM);
+  griddep_wait();
+  stamp.started();
+  griddep_launch();
+  FewItem it;
+  if (!find_few(p, blockIdx.y, &it)) return;
+  if (it.cnt <= 8) few_chunk<1>(p, it.e, it.row, it.cnt, blockIdx.x * F8F_ROWS, red);
+  else few_chunk<F8F_CHUNK / 8>(p, it.e, it.row, it.cnt, blockIdx.x * F8F_ROWS, red);
+}
+
 }  // namespace moe
