@@ -36,6 +36,7 @@ constexpr int F8G_STORE_WARPS = 8;
 constexpr int F8G_STG = F8G_STORE_WARPS * 4096;  // staging of 32 rows x 128 bytes per storing warp
 constexpr int F8G_SF_BUFS = 4;       // scale buffers ...
 constexpr int F8G_SF_K = 4;          // ... of four K blocks
+constexpr int F8G_SF_BYTES = 2 * 384 * 4;  // their words on the way to TMEM
 
 struct F8Gemm {
   CUtensorMap ma, mb;
@@ -55,7 +56,7 @@ inline int f8g_tile_n(int n) {
   return ((n + tiles - 1) / tiles + 15) / 16 * 16;
 }
 inline size_t f8g_fixed_bytes(int E) {
-  return 1024 + (size_t)F8G_STG + 256 + (size_t)(2 * E + 2 + F8G_THREADS / 32 + 1) * sizeof(int);
+  return 1024 + (size_t)F8G_STG + 256 + F8G_SF_BYTES + (size_t)(2 * E + 2 + F8G_THREADS / 32 + 1) * sizeof(int);
 }
 inline int f8g_stage_bytes(int tn, int kpb) { return (16384 + tn * 64) * kpb; }
 inline int f8g_stages(int E, int tn, int kpb) {
@@ -158,6 +159,19 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *r) {
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+// Barrier of warps 0 .. 3: true when all 128 threads passed true.
+__device__ __forceinline__ bool bar_all_128(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ bool f8_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                              uint64_t limit, long long info) {
   bool ok = true;
@@ -184,9 +198,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
   uint64_t *bars = (uint64_t *)(stg_all + F8G_STG);
   uint32_t *tmem_slot = (uint32_t *)(bars + 2 * NST + 5 + 2 * F8G_SF_BUFS);
   volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
-  int *prefix = (int *)(stg_all + F8G_STG + 256);
+  int *prefix = (int *)(stg_all + F8G_STG + 256 + F8G_SF_BYTES);
   int *start = prefix + p.E + 1;
   int *scan_tmp = start + p.E + 1;
+  uint32_t *sf_words = (uint32_t *)(stg_all + F8G_STG + 256);  // [2][A 128, B 256]
 
   auto full_bar = [&](int s) { return smem_u32(bars + s); };
   auto empty_bar = [&](int s) { return smem_u32(bars + NST + s); };
@@ -221,63 +236,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  if (tid == 32 * 12) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&p.ma) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&p.mb) : "memory");
+  }
+  // all of this before the grid wait, so that it overlaps the previous kernel's end
   const KernelStamp stamp(WGRAD ? K_F8B_WGRAD : K_F8B_GEMM);
-  griddep_wait();
-  stamp.started();
-  griddep_launch();
-  const int total = f8_tile_prefix<WGRAD>(p, prefix, start, scan_tmp);
+  const uint64_t limit = g_wait_limit_ns;
   tc_fence_before();
   cluster_sync_all();  // barriers of both CTAs initialised, TMEM allocated in both
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const uint64_t limit = g_wait_limit_ns;
+  griddep_wait();
+  stamp.started();
+  griddep_launch();
+  const int total = f8_tile_prefix<WGRAD>(p, prefix, start, scan_tmp);
   // scale buffer i (0 .. 3): 16 columns, 4 for A then up to 8 for B
   auto sf_col = [&](int i) { return tmem_base + (uint32_t)(256 * (i >> 1) + F8G_N + 16 * (i & 1)); };
 
   if (warp < 4) {
     // ------------------------------------------------------------ scales (both CTAs)
-    // Unit: up to four K blocks of a tile, read one unit ahead of the buffer's release.
-    const int nkb = (p.K + QB - 1) / QB, nnb = (p.N + QB - 1) / QB, nw = (p.tn + 31) / 32;
-    int tile = pair, kb = 0;
-    F8Tile t;
-    const uint8_t *pa[4];  // scales of rows 32 i + lane of this CTA's 128
-    bool oa[4];
-    auto enter = [&]() {
+    // Unit: up to four K blocks of a tile. Each of the 128 threads reads the bytes of one row of A and
+    // two of B, one unit ahead, and hands them to all four warps through shared memory.
+    const int nkb = (p.K + QB - 1) / QB, nnb = (p.N + QB - 1) / QB;
+    const bool word_a = !WGRAD && nkb % 4 == 0 && ((uintptr_t)p.a_scale & 3u) == 0;
+    const bool word_b = !WGRAD && nkb % 4 == 0 && ((uintptr_t)p.b_scale & 3u) == 0;
+    int tile = pair, kb = 0, nk = 0;
+    const uint8_t *src[3];
+    bool on[3];
+    auto enter = [&]() {  // the next tile that has K blocks
+      F8Tile t;
       for (; tile < total; tile += npairs) {
         t = f8_decode<WGRAD>(p, tile, prefix, start);
         if (t.nk > 0) break;
       }
-      kb = 0;
       if (tile >= total) return;
+      kb = 0;
+      nk = t.nk;
+      const int r = t.m0 + (int)rank * 128 + tid;
+      on[0] = r < t.rows;
+      src[0] = WGRAD ? p.a_scale + (size_t)t.kofs * p.M + r : p.a_scale + (size_t)(t.row0 + r) * nkb;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = t.m0 + (int)rank * 128 + 32 * i + lane;
-        oa[i] = r < t.rows;
-        pa[i] = WGRAD ? p.a_scale + (size_t)t.kofs * p.M + r : p.a_scale + (size_t)(t.row0 + r) * nkb;
+      for (int i = 0; i < 2; ++i) {
+        const int c = t.n0 + 128 * i + tid;
+        on[1 + i] = 128 * i + tid < p.tn && c < p.N;
+        src[1 + i] = WGRAD ? p.b_scale + (size_t)t.kofs * p.N + c
+                           : p.b_scale + ((size_t)t.g * nnb + c / QB) * nkb;
       }
     };
-    // the next unit's bytes of 4 rows of A and up to 8 of B (one word each where the bytes of four
-    // K blocks are one aligned word); columns past N and K blocks past the last read as 0
-    uint32_t w[12][F8G_SF_K];
-    const bool va = !WGRAD && nkb % 4 == 0 && ((uintptr_t)p.a_scale & 3u) == 0;
-    const bool vb = !WGRAD && nkb % 4 == 0 && ((uintptr_t)p.b_scale & 3u) == 0;
+    // the bytes of K blocks kb .. kb + 3 (as one word in w[.][0] where they are one aligned word);
+    // rows and columns past the last, and K blocks past the last, read as 0
+    uint32_t w[3][F8G_SF_K];
     auto fetch = [&]() {
 #pragma unroll
-      for (int i = 0; i < 12; ++i) {
-        const int c = t.n0 + 32 * (i - 4) + lane;
-        const bool on = i < 4 ? oa[i < 4 ? i : 0] : i - 4 < nw && c < p.N;
-        const uint8_t *src = i < 4 ? pa[i < 4 ? i : 0]
-                             : WGRAD ? p.b_scale + (size_t)t.kofs * p.N + c
-                                     : p.b_scale + ((size_t)t.g * nnb + c / QB) * nkb;
-        const size_t step = WGRAD ? (size_t)(i < 4 ? p.M : p.N) : 1;
-        const bool word = i < 4 ? va : vb;
+      for (int i = 0; i < 3; ++i) {
 #pragma unroll
         for (int j = 0; j < F8G_SF_K; ++j) w[i][j] = 0u;
-        if (on && word) w[i][0] = __ldg((const uint32_t *)(src + kb));
-        if (on && !word)
+        if (!on[i]) continue;
+        if (i == 0 ? word_a : word_b) {
+          w[i][0] = __ldg((const uint32_t *)(src[i] + kb));
+          continue;
+        }
 #pragma unroll
-          for (int j = 0; j < F8G_SF_K; ++j)
-            if (kb + j < t.nk) w[i][j] = __ldg(src + (size_t)(kb + j) * step);
+        for (int j = 0; j < F8G_SF_K; ++j)
+          if (kb + j < nk) w[i][j] = __ldg(src[i] + (size_t)(kb + j) * (WGRAD ? (i == 0 ? p.M : p.N) : 1));
       }
     };
     enter();
@@ -286,17 +308,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
     int unit = 0;
     uint32_t phase = 0;
     while (tile < total) {
-      uint32_t v[12];
+      uint32_t *mine = sf_words + (unit & 1) * 384;
 #pragma unroll
-      for (int i = 0; i < 12; ++i) v[i] = w[i][0] | w[i][1] << 8 | w[i][2] << 16 | w[i][3] << 24;
+      for (int i = 0; i < 3; ++i) mine[128 * i + tid] = w[i][0] | w[i][1] << 8 | w[i][2] << 16 | w[i][3] << 24;
       kb += F8G_SF_K;
-      if (kb >= t.nk) {
+      if (kb >= nk) {
         tile += npairs;
         enter();
       }
       if (tile < total) fetch();
-      if (!f8_wait_warp(sfe_bar(unit), phase ^ 1u, abort_flag, limit, INFO_WAIT_MMA_EMPTY)) break;
+      // released by the tensor core, and the words of all four warps written; all four leave together
+      if (!bar_all_128(f8_wait_warp(sfe_bar(unit), phase ^ 1u, abort_flag, limit, INFO_WAIT_MMA_EMPTY))) break;
       tc_fence_after();
+      uint32_t v[12];
+#pragma unroll
+      for (int i = 0; i < 12; ++i) v[i] = mine[32 * i + lane];
       tmem_st4(sf_col(unit) + quarter, v);
       tmem_st8(sf_col(unit) + 4 + quarter, v + 4);
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
