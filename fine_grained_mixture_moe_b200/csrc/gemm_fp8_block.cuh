@@ -46,6 +46,8 @@ struct F8Gemm {
   long long rows;          // rows of a (gemm) or grouped rows (wgrad)
   int E, M, N, K;          // gemm: N = n, K = k; wgrad: M = n, N = k, K = blocks the buffers hold
   int tn;                  // columns per tile, a multiple of 16 up to F8G_N
+  int nt;                  // column tiles
+  unsigned nt_mul;         // floor(2^32 / nt) + 1: x / nt = umulhi(x, nt_mul), or one less (nt > 1)
   int out_f32;
   int stages, kpb;
 };
@@ -75,7 +77,7 @@ struct F8Tile {
 // (gemm) or first K blocks (wgrad).
 template <bool WGRAD>
 __device__ __forceinline__ int f8_tile_prefix(const F8Gemm &p, int *prefix, int *start, int *tmp) {
-  const int nt = (p.N + p.tn - 1) / p.tn;
+  const int nt = p.nt;
   for (int g = threadIdx.x; g <= p.E; g += blockDim.x) {
     const long long a = p.offsets ? expert_bound(p.offsets, g, p.rows) : g ? p.rows : 0;
     long long n = 0;
@@ -119,12 +121,16 @@ __device__ __forceinline__ int f8_blocks(const F8Gemm &p, int tile, const int *p
 
 template <bool WGRAD>
 __device__ __forceinline__ F8Tile f8_decode(const F8Gemm &p, int tile, const int *prefix, const int *start) {
-  const int nt = (p.N + p.tn - 1) / p.tn;
   F8Tile t;
   t.g = f8_group(p, tile, prefix);
   const int local = tile - prefix[t.g];
-  t.m0 = (local / nt) * 256;
-  t.n0 = (local % nt) * p.tn;
+  int row = local;  // row and column of the tile: local / nt without a division
+  if (p.nt > 1) {
+    row = (int)__umulhi((unsigned)local, p.nt_mul);
+    if (row * p.nt > local) --row;
+  }
+  t.m0 = row * 256;
+  t.n0 = (local - row * p.nt) * p.tn;
   if (WGRAD) {
     t.rows = p.M;
     t.row0 = (long long)t.g * p.M;
