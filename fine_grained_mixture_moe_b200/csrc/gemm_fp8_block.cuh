@@ -464,7 +464,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
       unsigned char *out = (unsigned char *)p.out + ((size_t)(t.row0 + rbase) * p.N + t.n0) * ebytes;
       const size_t pitch = (size_t)p.N * ebytes;
       // the two warps of a lane quarter take every other pass: 32 rows of the staging buffer, written
-      // lane = row, read 8 lanes per row (whole 128-byte lines)
+      // lane = row, read 8 lanes per row (whole 128-byte lines);
+      // streaming stores, so that the operands stay in L2 (35.0 us instead of 36.0, Quartz gate|up)
       if (nrows > 0)
         for (int c = half * cpp; c < ncols; c += 2 * cpp) {
           if (p.out_f32) {
@@ -502,8 +503,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
           for (int i = 0; i < 8; ++i) {
             const int rr = 4 * i + (lane >> 3), ch = lane & 7;
             if (rr < nrows && c + ch * (cpp >> 3) < ncols)
-              *(uint4 *)(out + rr * pitch + (size_t)c * ebytes + ch * 16) =
-                  *(const uint4 *)(stg + rr * 128 + ((ch ^ (rr & 7)) << 4));
+              __stcs((uint4 *)(out + rr * pitch + (size_t)c * ebytes + ch * 16),
+                     *(const uint4 *)(stg + rr * 128 + ((ch ^ (rr & 7)) << 4)));
           }
           __syncwarp();
         }
