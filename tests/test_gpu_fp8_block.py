@@ -156,6 +156,31 @@ def test_quantize_tokens(dtype, R, E, C, kind):
     assert (np8(s)[n:] == 0xAA).all() and (np8(q)[:, 128 * n:] == 0xAA).all()
 
 
+@pytest.mark.parametrize("span", [0, 3, 15, 16, 40])
+@pytest.mark.parametrize("R,E", [(128, 1), (300, 3)])
+def test_quantize_tokens_from_codes_of_any_size(span, R, E):
+    """Every code magnitude, from columns of the least subnormal to columns of 448, under row scales
+    that span 2^span (up to 2^15 the kernel works in fp16), with zero rows and zero columns."""
+    rng = np.random.default_rng(span + R)
+    C = 144
+    top = np.minimum(np.arange(C) % 128, 126)            # column c holds codes up to `top`
+    q0 = (rng.integers(0, 1 << 30, (R, C)) % (top + 1)).astype(np.uint8)
+    q0 |= (rng.integers(0, 2, (R, C)) << 7).astype(np.uint8)
+    q0[5] = 0
+    s0 = (120 - rng.integers(0, span + 1, (R, 2))).astype(np.uint8)
+    s0[0], s0[1] = 120, 120 - span
+    offs = splits("skew" if E > 1 else "even", R, E, rng)
+    nb = B.moe_fp8_token_blocks(R, E)
+    q, s = u8(C, 128 * nb), u8(nb, C)
+    B.moe_quantize_fp8_tokens(torch.from_numpy(q0).to(DEV), torch.from_numpy(s0).to(DEV), R, C,
+                              torch.from_numpy(offs).to(DEV), E, q, s)
+    check_device()
+    rq, rs = FB.quantize_tokens(FB.values_rows(q0, s0), offs)
+    n = rs.shape[0]
+    assert np.array_equal(np8(s)[:n], rs)
+    assert np.array_equal(np8(q)[:, :128 * n], rq)
+
+
 # ------------------------------------------------------------------ products
 def product_tol(ref, mag, K, dtype):
     return (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * np.abs(ref) \
