@@ -348,59 +348,62 @@ def _nblocks(n: int) -> int:
 
 
 class _Fp8Types:
-    """Accepted types by role, and DTYPE codes; built once, on the first call."""
+    """Accepted types by role, DTYPE codes and torch's device queries; built once, on first use."""
 
     def __init__(self):
         import torch
-        self.torch = torch
         self.code = (torch.uint8, torch.float8_e4m3fn)
         self.scale = (torch.uint8, torch.float8_e8m0fnu)
         self.value = (torch.bfloat16, torch.float32)
+        self.any = self.value + self.code
         self.i32, self.bf16, self.f32 = (torch.int32,), (torch.bfloat16,), (torch.float32,)
         self.dtype = {torch.bfloat16: DTYPE["bf16"], torch.float32: DTYPE["f32"],
                       torch.uint8: DTYPE["e4m3"], torch.float8_e4m3fn: DTYPE["e4m3"]}
+        self.cuda = torch.cuda
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 _fp8_types: Optional[_Fp8Types] = None
 
 
-class _Fp8Call:
-    """Checks and converts the arguments of one call: a small call's time is mostly the host's."""
-    __slots__ = ("fn", "ty", "device")
+def _fp8():
+    """The types, and the current CUDA device (0 before CUDA is up: host tensors are refused)."""
+    global _fp8_types
+    if _fp8_types is None:
+        _fp8_types = _Fp8Types()
+    cuda = _fp8_types.cuda
+    return _fp8_types, cuda.current_device() if cuda.is_initialized() else 0
 
-    def __init__(self, fn: str):
-        global _fp8_types
-        if _fp8_types is None:
-            _fp8_types = _Fp8Types()
-        self.fn = fn
-        self.ty = _fp8_types
-        cuda = self.ty.torch.cuda
-        self.device = cuda.current_device() if cuda.is_initialized() else 0
 
-    def __call__(self, name: str, t, dtypes, numel: int) -> Optional[int]:
-        if t is None or type(t) is int:
-            return t
-        if t.dtype not in dtypes:
-            raise TypeError(f"{self.fn}: {name} has dtype {t.dtype}, expected one of {dtypes}")
-        if t.numel() < numel:
-            raise ValueError(f"{self.fn}: {name} has {t.numel()} elements, needs {numel}")
-        if not t.is_contiguous():
-            raise ValueError(f"{self.fn}: {name} is not contiguous")
-        if t.get_device() != self.device:  # -1 for a host tensor
-            raise ValueError(f"{self.fn}: {name} is on {t.device}, not on the current CUDA device")
+def _buf(fn: str, name: str, t, dtypes, numel: int, dev: int) -> Optional[int]:
+    """Address of a tensor that may be an argument (a small call's time is mostly the host's, so the
+    good case is one chain of tests)."""
+    if t is None or type(t) is int:
+        return t
+    if t.dtype in dtypes and t.numel() >= numel and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
+    if t.dtype not in dtypes:
+        raise TypeError(f"{fn}: {name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.numel() < numel:
+        raise ValueError(f"{fn}: {name} has {t.numel()} elements, needs {numel}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} is not contiguous")
+    raise ValueError(f"{fn}: {name} is on {t.device}, not on the current CUDA device")
 
-    def stream(self, stream) -> Optional[int]:
-        return _stream(stream) if stream is not None else \
-            self.ty.torch._C._cuda_getCurrentRawStream(self.device)
 
-    def dtype(self, name: str, t) -> int:
-        """DTYPE code of a tensor of values or codes."""
-        code = self.ty.dtype.get(getattr(t, "dtype", None))
-        if code is None:
-            raise TypeError(f"{self.fn}: {name} must be a bf16, fp32 or E4M3 tensor, got "
-                            f"{getattr(t, 'dtype', type(t))}")
-        return code
+def _code_of(fn: str, name: str, t, ty) -> int:
+    """DTYPE code of a tensor whose type selects the call's."""
+    code = ty.dtype.get(getattr(t, "dtype", None))
+    if code is None:
+        raise TypeError(f"{fn}: {name} must be a bf16, fp32 or E4M3 tensor, got "
+                        f"{getattr(t, 'dtype', type(t))}")
+    return code
+
+
+def _stream_of(stream, ty, dev: int) -> Optional[int]:
+    if stream is None and ty.raw_stream is not None:
+        return ty.raw_stream(dev)
+    return _stream(stream)
 
 
 def moe_fp8_token_blocks(rows: int, E: int) -> int:
@@ -413,94 +416,102 @@ def moe_fp8_token_blocks(rows: int, E: int) -> int:
 
 def moe_quantize_fp8_block(x, rows: int, cols: int, q, scale, n_rows=None, stream=None) -> None:
     """E4M3 codes q [rows, cols] and E8M0 scales [rows, ceil(cols / 128)] of x (bf16 or fp32)."""
-    buf = _Fp8Call("moe_quantize_fp8_block")
-    ty = buf.ty
-    _check(buf.fn, load().moe_quantize_fp8_block(
-        buf("x", x, ty.value, rows * cols), buf.dtype("x", x), rows, cols,
-        buf("n_rows", n_rows, ty.i32, 1), buf("q", q, ty.code, rows * cols),
-        buf("scale", scale, ty.scale, rows * _nblocks(cols)), buf.stream(stream)))
+    fn = "moe_quantize_fp8_block"
+    ty, dev = _fp8()
+    _check(fn, load().moe_quantize_fp8_block(
+        _buf(fn, "x", x, ty.value, rows * cols, dev), _code_of(fn, "x", x, ty), rows, cols,
+        _buf(fn, "n_rows", n_rows, ty.i32, 1, dev), _buf(fn, "q", q, ty.code, rows * cols, dev),
+        _buf(fn, "scale", scale, ty.scale, rows * _nblocks(cols), dev),
+        _stream_of(stream, ty, dev)))
 
 
 def moe_quantize_fp8_weight(w, E: int, rows: int, cols: int, q, scale, q_t=None, scale_t=None,
                             stream=None) -> None:
     """Codes and scales of stacked weights w [E, rows, cols] in 128 x 128 blocks, and optionally of
     the transposed weights."""
-    buf = _Fp8Call("moe_quantize_fp8_weight")
-    ty = buf.ty
+    fn = "moe_quantize_fp8_weight"
+    ty, dev = _fp8()
     n, nb = E * rows * cols, E * _nblocks(rows) * _nblocks(cols)
-    _check(buf.fn, load().moe_quantize_fp8_weight(
-        buf("w", w, ty.value, n), buf.dtype("w", w), E, rows, cols,
-        buf("q", q, ty.code, n), buf("scale", scale, ty.scale, nb),
-        buf("q_t", q_t, ty.code, n), buf("scale_t", scale_t, ty.scale, nb),
-        buf.stream(stream)))
+    _check(fn, load().moe_quantize_fp8_weight(
+        _buf(fn, "w", w, ty.value, n, dev), _code_of(fn, "w", w, ty), E, rows, cols,
+        _buf(fn, "q", q, ty.code, n, dev), _buf(fn, "scale", scale, ty.scale, nb, dev),
+        _buf(fn, "q_t", q_t, ty.code, n, dev), _buf(fn, "scale_t", scale_t, ty.scale, nb, dev),
+        _stream_of(stream, ty, dev)))
 
 
 def moe_quantize_fp8_tokens(x, x_scale, rows: int, cols: int, offsets, E: int, q_t, scale_t,
                             stream=None) -> None:
-    """Transposed codes q_t [cols, 128 B] and scales [B, cols] along each expert's rows, from bf16 or
-    fp32 rows (x_scale None) or from E4M3 rows with their scales; B = moe_fp8_token_blocks."""
-    buf = _Fp8Call("moe_quantize_fp8_tokens")
-    ty = buf.ty
+    """Transposed codes q_t [cols, 128 B] and scales [B, cols] along each expert's rows, from bf16
+    or fp32 rows (x_scale None) or from E4M3 rows with their scales; B = moe_fp8_token_blocks."""
+    fn = "moe_quantize_fp8_tokens"
+    ty, dev = _fp8()
     nb = moe_fp8_token_blocks(rows, E)
-    _check(buf.fn, load().moe_quantize_fp8_tokens(
-        buf("x", x, ty.value + ty.code, rows * cols), buf.dtype("x", x),
-        buf("x_scale", x_scale, ty.scale, rows * _nblocks(cols)), rows, cols,
-        buf("offsets", offsets, ty.i32, E + 1), E,
-        buf("q_t", q_t, ty.code, cols * BLOCK * nb),
-        buf("scale_t", scale_t, ty.scale, nb * cols), buf.stream(stream)))
+    _check(fn, load().moe_quantize_fp8_tokens(
+        _buf(fn, "x", x, ty.any, rows * cols, dev), _code_of(fn, "x", x, ty),
+        _buf(fn, "x_scale", x_scale, ty.scale, rows * _nblocks(cols), dev), rows, cols,
+        _buf(fn, "offsets", offsets, ty.i32, E + 1, dev), E,
+        _buf(fn, "q_t", q_t, ty.code, cols * BLOCK * nb, dev),
+        _buf(fn, "scale_t", scale_t, ty.scale, nb * cols, dev), _stream_of(stream, ty, dev)))
 
 
 def moe_gemm_fp8_block(a, a_scale, rows: int, offsets, E: int, n: int, k: int, w, w_scale, out,
                        stream=None) -> None:
     """out [rows, n] (bf16 or fp32) = a [rows, k] w[e]^T, expert e's rows by offsets."""
-    buf = _Fp8Call("moe_gemm_fp8_block")
-    ty = buf.ty
-    _check(buf.fn, load().moe_gemm_fp8_block(
-        buf("a", a, ty.code, rows * k), buf("a_scale", a_scale, ty.scale, rows * _nblocks(k)),
-        rows, buf("offsets", offsets, ty.i32, E + 1), E, n, k,
-        buf("w", w, ty.code, E * n * k),
-        buf("w_scale", w_scale, ty.scale, E * _nblocks(n) * _nblocks(k)),
-        buf("out", out, ty.value, rows * n), buf.dtype("out", out), buf.stream(stream)))
+    fn = "moe_gemm_fp8_block"
+    ty, dev = _fp8()
+    _check(fn, load().moe_gemm_fp8_block(
+        _buf(fn, "a", a, ty.code, rows * k, dev),
+        _buf(fn, "a_scale", a_scale, ty.scale, rows * _nblocks(k), dev),
+        rows, _buf(fn, "offsets", offsets, ty.i32, E + 1, dev), E, n, k,
+        _buf(fn, "w", w, ty.code, E * n * k, dev),
+        _buf(fn, "w_scale", w_scale, ty.scale, E * _nblocks(n) * _nblocks(k), dev),
+        _buf(fn, "out", out, ty.value, rows * n, dev),
+        _code_of(fn, "out", out, ty), _stream_of(stream, ty, dev)))
 
 
 def moe_wgrad_fp8_block(a_t, a_scale, b_t, b_scale, rows: int, offsets, E: int, n: int, k: int, dw,
                         stream=None) -> None:
-    """dw [E, n, k] (fp32) = per expert a^T b, both operands as moe_quantize_fp8_tokens wrote them."""
-    buf = _Fp8Call("moe_wgrad_fp8_block")
-    ty = buf.ty
+    """dw [E, n, k] (fp32) = per expert a^T b, both operands from moe_quantize_fp8_tokens."""
+    fn = "moe_wgrad_fp8_block"
+    ty, dev = _fp8()
     nb = moe_fp8_token_blocks(rows, E)
-    _check(buf.fn, load().moe_wgrad_fp8_block(
-        buf("a_t", a_t, ty.code, n * BLOCK * nb), buf("a_scale", a_scale, ty.scale, nb * n),
-        buf("b_t", b_t, ty.code, k * BLOCK * nb), buf("b_scale", b_scale, ty.scale, nb * k),
-        rows, buf("offsets", offsets, ty.i32, E + 1), E, n, k,
-        buf("dw", dw, ty.f32, E * n * k), buf.stream(stream)))
+    _check(fn, load().moe_wgrad_fp8_block(
+        _buf(fn, "a_t", a_t, ty.code, n * BLOCK * nb, dev),
+        _buf(fn, "a_scale", a_scale, ty.scale, nb * n, dev),
+        _buf(fn, "b_t", b_t, ty.code, k * BLOCK * nb, dev),
+        _buf(fn, "b_scale", b_scale, ty.scale, nb * k, dev),
+        rows, _buf(fn, "offsets", offsets, ty.i32, E + 1, dev), E, n, k,
+        _buf(fn, "dw", dw, ty.f32, E * n * k, dev), _stream_of(stream, ty, dev)))
 
 
 def moe_swiglu_fp8_forward(gu, rows: int, ffn: int, h=None, h_q=None, h_scale=None, gu_q=None,
                            gu_scale=None, n_rows=None, stream=None) -> None:
     """h = silu(gate) * up of gu [rows, 2 ffn] in bf16 (h) and / or E4M3 (h_q, h_scale), and gu's own
     E4M3 checkpoint (gu_q, gu_scale)."""
-    buf = _Fp8Call("moe_swiglu_fp8_forward")
-    ty = buf.ty
+    fn = "moe_swiglu_fp8_forward"
+    ty, dev = _fp8()
     n, nb = rows * ffn, rows * _nblocks(ffn)
-    _check(buf.fn, load().moe_swiglu_fp8_forward(
-        buf("gu", gu, ty.value, 2 * n), buf.dtype("gu", gu), rows, ffn,
-        buf("n_rows", n_rows, ty.i32, 1), buf("h", h, ty.bf16, n),
-        buf("h_q", h_q, ty.code, n), buf("h_scale", h_scale, ty.scale, nb),
-        buf("gu_q", gu_q, ty.code, 2 * n), buf("gu_scale", gu_scale, ty.scale, 2 * nb),
-        buf.stream(stream)))
+    _check(fn, load().moe_swiglu_fp8_forward(
+        _buf(fn, "gu", gu, ty.value, 2 * n, dev), _code_of(fn, "gu", gu, ty), rows, ffn,
+        _buf(fn, "n_rows", n_rows, ty.i32, 1, dev), _buf(fn, "h", h, ty.bf16, n, dev),
+        _buf(fn, "h_q", h_q, ty.code, n, dev), _buf(fn, "h_scale", h_scale, ty.scale, nb, dev),
+        _buf(fn, "gu_q", gu_q, ty.code, 2 * n, dev),
+        _buf(fn, "gu_scale", gu_scale, ty.scale, 2 * nb, dev),
+        _stream_of(stream, ty, dev)))
 
 
 def moe_swiglu_fp8_backward(gu_q, gu_scale, dh, rows: int, ffn: int, dgu=None, dgu_q=None,
                             dgu_scale=None, h=None, n_rows=None, stream=None) -> None:
     """[d_gate | d_up] [rows, 2 ffn] in bf16 (dgu) and / or E4M3 (dgu_q, dgu_scale), and h again in
     bf16, from the checkpoint gu_q, gu_scale and dh [rows, ffn]."""
-    buf = _Fp8Call("moe_swiglu_fp8_backward")
-    ty = buf.ty
+    fn = "moe_swiglu_fp8_backward"
+    ty, dev = _fp8()
     n, nb = rows * ffn, rows * _nblocks(ffn)
-    _check(buf.fn, load().moe_swiglu_fp8_backward(
-        buf("gu_q", gu_q, ty.code, 2 * n), buf("gu_scale", gu_scale, ty.scale, 2 * nb),
-        buf("dh", dh, ty.value, n), buf.dtype("dh", dh), rows, ffn,
-        buf("n_rows", n_rows, ty.i32, 1), buf("dgu", dgu, ty.bf16, 2 * n),
-        buf("dgu_q", dgu_q, ty.code, 2 * n), buf("dgu_scale", dgu_scale, ty.scale, 2 * nb),
-        buf("h", h, ty.bf16, n), buf.stream(stream)))
+    _check(fn, load().moe_swiglu_fp8_backward(
+        _buf(fn, "gu_q", gu_q, ty.code, 2 * n, dev),
+        _buf(fn, "gu_scale", gu_scale, ty.scale, 2 * nb, dev),
+        _buf(fn, "dh", dh, ty.value, n, dev), _code_of(fn, "dh", dh, ty), rows, ffn,
+        _buf(fn, "n_rows", n_rows, ty.i32, 1, dev), _buf(fn, "dgu", dgu, ty.bf16, 2 * n, dev),
+        _buf(fn, "dgu_q", dgu_q, ty.code, 2 * n, dev),
+        _buf(fn, "dgu_scale", dgu_scale, ty.scale, 2 * nb, dev),
+        _buf(fn, "h", h, ty.bf16, n, dev), _stream_of(stream, ty, dev)))
