@@ -209,6 +209,29 @@ __device__ __forceinline__ uint32_t block_byte(uint32_t lane_amax) {
   return e8m0_of_amax(team_max<RT_LANES>(lane_amax));
 }
 
+// A lane's offset in rows of `pitch` elements that start with `nb` blocks, walked in flat block order
+// (block b is block b % nb of row b / nb) without a division per step. SwiGLU: the gate blocks of
+// [., 2 f] rows; the up columns are f further.
+struct FlatWalk {
+  long long off, doff;
+  int blk, nb, dblk, wrap;
+  __device__ __forceinline__ FlatWalk(const RowTeam &w, int nb_, int pitch) : nb(nb_), wrap(pitch - nb_ * QB) {
+    const long long b = w.first + w.team, row = b / nb, drow = w.step / nb;
+    blk = (int)(b - row * nb);
+    off = row * pitch + blk * QB + w.c;
+    dblk = (int)(w.step - drow * nb);
+    doff = drow * pitch + dblk * QB;
+  }
+  __device__ __forceinline__ void next() {
+    off += doff;
+    blk += dblk;
+    if (blk >= nb) {  // the next row, nb blocks back
+      blk -= nb;
+      off += wrap;
+    }
+  }
+};
+
 // ------------------------------------------------------------------ rows, 1 x 128 blocks
 constexpr int F8Q_U = 2;  // blocks in flight per team: 64 bytes per lane, which HBM's latency asks for
 
@@ -225,6 +248,7 @@ __global__ void __launch_bounds__(256, 4)
   griddep_launch();
   const RowTeam w;
   const long long total = valid_rows(rows, n_rows) * nblk;
+  FlatWalk at(w, nblk, cols);
   for (long long b0 = w.first; b0 < total; b0 += U * w.step) {
     Lane16<Tin> x[U];
     long long off[U];
@@ -236,11 +260,10 @@ __global__ void __launch_bounds__(256, 4)
       if (FULL) {
         off[u] = b * QB + w.c;
       } else {
-        const long long row = b / nblk;
-        const int col = (int)(b - row * nblk) * QB + w.c;
-        off[u] = row * cols + col;
-        ok[u][0] &= col < cols;
-        ok[u][1] &= col + 64 < cols;
+        off[u] = at.off;
+        ok[u][0] &= at.blk * QB + w.c < cols;
+        ok[u][1] &= at.blk * QB + w.c + 64 < cols;
+        at.next();
       }
       x[u].zero();
       if (ok[u][0]) x[u].p[0].load(in + off[u]);
@@ -517,31 +540,6 @@ __device__ __forceinline__ float sigmoid_f(float z) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return r;
 }
-// Walk over the blocks of h [., f] in flat order and the offsets of their gate columns in
-// [., 2 f] rows (the up columns are f further): no division per step.
-struct GateWalk {
-  long long gate;  // offset of this lane's gate columns
-  int blk, nb, dblk;
-  long long dgate;
-  int f;
-  __device__ __forceinline__ GateWalk(const RowTeam &w, int f_) : nb(f_ / QB), f(f_) {
-    const long long b = w.first + w.team, row = b / nb;
-    blk = (int)(b - row * nb);
-    gate = row * 2 * f + blk * QB + w.c;
-    const long long drow = w.step / nb;
-    dblk = (int)(w.step - drow * nb);
-    dgate = drow * 2 * f + dblk * QB;
-  }
-  __device__ __forceinline__ void next() {
-    gate += dgate;
-    blk += dblk;
-    if (blk >= nb) {  // the next row, nb blocks back
-      blk -= nb;
-      gate += f;
-    }
-  }
-};
-
 // gu [rows, 2 f] = [gate | up]: h = silu(g) u, to h (bf16) and / or h_q + h_scale (the down product's
 // operand, quantised from the fp32 value), and the E4M3 codes of gu itself to gu_q + gu_scale (the
 // checkpoint of the backward pass). f a multiple of 128, so no block spans gate and up.
@@ -556,7 +554,7 @@ __global__ void __launch_bounds__(256, 4)
   stamp.started();
   griddep_launch();
   const RowTeam w;
-  GateWalk at(w, f);
+  FlatWalk at(w, f / QB, 2 * f);
   const long long total = valid_rows(rows, n_rows) * at.nb;
   for (long long b0 = w.first; b0 < total; b0 += w.step, at.next()) {
     const long long b = b0 + w.team, off = b * QB + w.c;  // in h
@@ -565,8 +563,8 @@ __global__ void __launch_bounds__(256, 4)
     xg.zero();
     xu.zero();
     if (ok) {
-      xg.load(gu + at.gate);
-      xu.load(gu + at.gate + f);
+      xg.load(gu + at.off);
+      xu.load(gu + at.off + f);
     }
     uint32_t bg = 0, bu = 0;
     if (gu_q) {
@@ -574,8 +572,8 @@ __global__ void __launch_bounds__(256, 4)
       bu = block_byte(xu.amax());
       // the gate block's scale sits where the block does, in rows of 2 nb
       if (ok && w.c == 0) {
-        gu_scale[at.gate / QB] = (uint8_t)bg;
-        gu_scale[at.gate / QB + at.nb] = (uint8_t)bu;
+        gu_scale[at.off / QB] = (uint8_t)bg;
+        gu_scale[at.off / QB + at.nb] = (uint8_t)bu;
       }
     }
     float hv[2][8];
@@ -585,8 +583,8 @@ __global__ void __launch_bounds__(256, 4)
       xg.p[x].values(g);
       xu.p[x].values(u);
       if (gu_q && ok) {
-        store_codes(gu_q + at.gate + 64 * x, g, e8m0_inverse(bg));
-        store_codes(gu_q + at.gate + f + 64 * x, u, e8m0_inverse(bu));
+        store_codes(gu_q + at.off + 64 * x, g, e8m0_inverse(bg));
+        store_codes(gu_q + at.off + f + 64 * x, u, e8m0_inverse(bu));
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) hv[x][i] = g[i] * sigmoid_f(g[i]) * u[i];
@@ -619,7 +617,7 @@ __global__ void __launch_bounds__(256, 4)
   stamp.started();
   griddep_launch();
   const RowTeam w;
-  GateWalk at(w, f);
+  FlatWalk at(w, f / QB, 2 * f);
   const long long total = valid_rows(rows, n_rows) * at.nb;
   for (long long b0 = w.first; b0 < total; b0 += w.step, at.next()) {
     const long long b = b0 + w.team, off = b * QB + w.c;
@@ -632,12 +630,12 @@ __global__ void __launch_bounds__(256, 4)
     if (ok) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        cg[x] = __ldg((const uint2 *)(gu_q + at.gate + 64 * x));
-        cu[x] = __ldg((const uint2 *)(gu_q + at.gate + f + 64 * x));
+        cg[x] = __ldg((const uint2 *)(gu_q + at.off + 64 * x));
+        cu[x] = __ldg((const uint2 *)(gu_q + at.off + f + 64 * x));
       }
       xd.load(dh + off);
-      sg = __ldg(gu_scale + at.gate / QB);
-      su = __ldg(gu_scale + at.gate / QB + at.nb);
+      sg = __ldg(gu_scale + at.off / QB);
+      su = __ldg(gu_scale + at.off / QB + at.nb);
     }
     const float vg = e8m0_value(sg), vu = e8m0_value(su);
     float dg[2][8], du[2][8];
@@ -661,8 +659,8 @@ __global__ void __launch_bounds__(256, 4)
         }
       }
       if (ok && dgu) {
-        store_bf16x8(dgu + at.gate + 64 * x, dg[x]);
-        store_bf16x8(dgu + at.gate + f + 64 * x, du[x]);
+        store_bf16x8(dgu + at.off + 64 * x, dg[x]);
+        store_bf16x8(dgu + at.off + f + 64 * x, du[x]);
       }
       if (ok && h) store_bf16x8(h + off + 64 * x, hv);
     }
@@ -673,12 +671,12 @@ __global__ void __launch_bounds__(256, 4)
         const float ig = e8m0_inverse(bg), iu = e8m0_inverse(bu);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          store_codes(dgu_q + at.gate + 64 * x, dg[x], ig);
-          store_codes(dgu_q + at.gate + f + 64 * x, du[x], iu);
+          store_codes(dgu_q + at.off + 64 * x, dg[x], ig);
+          store_codes(dgu_q + at.off + f + 64 * x, du[x], iu);
         }
         if (w.c == 0) {
-          dgu_scale[at.gate / QB] = (uint8_t)bg;
-          dgu_scale[at.gate / QB + at.nb] = (uint8_t)bu;
+          dgu_scale[at.off / QB] = (uint8_t)bg;
+          dgu_scale[at.off / QB + at.nb] = (uint8_t)bu;
         }
       }
     }

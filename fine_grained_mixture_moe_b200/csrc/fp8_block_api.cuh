@@ -19,6 +19,9 @@
     if ((E) > 1024) return MOE_ERR_UNSUPPORTED; \
   } while (0)
 
+// tiles of one launch: a 32-bit tile number with room for one more stride
+#define MOE_F8B_TILES ((1ll << 31) - 65536)
+
 static inline bool f8b_dtype(int32_t t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32; }
 static inline bool aligned32(const void *p) { return p && ((uintptr_t)p & 31u) == 0; }
 static inline bool aligned4(const void *p) { return p && ((uintptr_t)p & 3u) == 0; }
@@ -83,7 +86,7 @@ moe_status_t moe_gemm_fp8_block(const uint8_t *a, const uint8_t *a_scale, int64_
   MOE_F8B_WIDTH(n);
   MOE_F8B_WIDTH(k);
   if (!f8b_dtype(out_dtype) || (long long)E * n > (1ll << 31) - 4096) return MOE_ERR_UNSUPPORTED;
-  if ((ceil_div(rows, 256) + (long long)E) * ceil_div(n, 256) > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
+  if ((ceil_div(rows, 256) + (long long)E) * ceil_div(n, f8g_tile_n(n)) > MOE_F8B_TILES) return MOE_ERR_UNSUPPORTED;
   MOE_REQUIRE(offsets || E == 1);
   if (rows == 0) return MOE_OK;
   MOE_REQUIRE(aligned16(a) && a_scale && aligned16(w) && w_scale && aligned32(out) &&
@@ -114,7 +117,7 @@ moe_status_t moe_wgrad_fp8_block(const uint8_t *a_t, const uint8_t *a_scale, con
   MOE_F8B_WIDTH(n);
   MOE_F8B_WIDTH(k);
   if (token_blocks(rows, E) > (1ll << 24) - 1) return MOE_ERR_UNSUPPORTED;  // K coordinates
-  if ((long long)E * ceil_div(n, 256) * ceil_div(k, 256) > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
+  if ((long long)E * ceil_div(n, 256) * ceil_div(k, f8g_tile_n(k)) > MOE_F8B_TILES) return MOE_ERR_UNSUPPORTED;
   MOE_REQUIRE(aligned32(dw));
   cudaStream_t st = (cudaStream_t)stream;
   if (rows == 0)

@@ -74,8 +74,10 @@ def test_gemm(lib):
     assert call(off=None) == INVALID                              # only one expert needs none
     assert call(E=1024, n=1 << 20, k=16, rows=1 << 30) == UNSUPPORTED
     for bad in (dict(a=None), dict(a=P + 8), dict(s=None), dict(w=None), dict(ws=None),
-                dict(out=P + 8), dict(off=P + 2)):
+                dict(out=P + 8), dict(out=P + 16), dict(off=P + 2)):
         assert call(**bad) == INVALID
+    # more tiles than a 32-bit tile number holds
+    assert call(rows=(1 << 31) - 4096, n=1 << 20, E=1, off=None) == UNSUPPORTED
 
 
 def test_wgrad(lib):
@@ -88,7 +90,7 @@ def test_wgrad(lib):
                  v["dw"], None)
     assert call(rows=-4) == INVALID and call(n=24) == UNSUPPORTED and call(E=-1) == INVALID
     for bad in (dict(a=None), dict(s=None), dict(b=P + 4), dict(bs=P + 1), dict(off=None),
-                dict(dw=None), dict(dw=P + 8)):
+                dict(dw=None), dict(dw=P + 8), dict(dw=P + 16)):
         assert call(**bad) == INVALID
 
 

@@ -218,6 +218,46 @@ def test_gemm(dtype, R, E, n, k, kind):
     assert (got[N:] == -7.0).all()
 
 
+@pytest.mark.parametrize("R,E,n,k", [(5000, 1, 16, 16), (4200, 3, 48, 144), (6000, 1024, 32, 80),
+                                     (300, 4, 640, 512)])
+def test_rows_before_the_first_expert(R, E, n, k):
+    """Offsets that start behind row 0 (and, from 4,097 rows, the tile form at its smallest widths):
+    the product, the token quantiser and the weight gradient agree on which rows an expert has."""
+    rng = np.random.default_rng(R)
+    offs = splits("skew", R - 40, E, rng) + 23
+    q, s = FB.quantize_rows(rng.standard_normal((R, k)))
+    q[:23] = 0x7F
+    q[R - 17:] = 0x7F
+    wq, ws = FB.quantize_weight(rng.standard_normal((E, n, k)))
+    d = [torch.from_numpy(a).to(DEV) for a in (q, s, offs.astype(np.int32), wq, ws)]
+    out = torch.full((R, n), -7.0, device=DEV)
+    B.moe_gemm_fp8_block(d[0], d[1], R, d[2], E, n, k, d[3], d[4], out)
+    check_device()
+    q[:23] = q[R - 17:] = 0
+    A, W = FB.values_rows(q, s), FB.values_weight(wq, ws)
+    ref, mag = FB.gemm(A, W, offs), FB.gemm(A, W, offs, absolute=True)
+    live = slice(23, R - 17)
+    got = out.cpu().numpy().astype(np.float64)
+    assert np.all(np.abs(got - ref)[live] <= product_tol(ref, mag, k, "f32")[live])
+    assert (got[:23] == -7.0).all() and (got[R - 17:] == -7.0).all()
+    nb = B.moe_fp8_token_blocks(R, E)
+    xq, xs = u8(k, 128 * nb), u8(nb, k)
+    B.moe_quantize_fp8_tokens(d[0], d[1], R, k, d[2], E, xq, xs)
+    dw = torch.full((E, k, k), -7.0, device=DEV)
+    if E <= 8:
+        B.moe_wgrad_fp8_block(xq, xs, xq, xs, R, d[2], E, k, k, dw)
+    check_device()
+    rq, rs = FB.quantize_tokens(A, offs)
+    m = rs.shape[0]
+    assert np.array_equal(np8(xs)[:m], rs) and np.array_equal(np8(xq)[:, :128 * m], rq)
+    if E <= 8:
+        vals = FB.values_tokens(rq, rs).T
+        V = np.zeros((R, k))
+        V[live] = np.concatenate([vals[128 * b:128 * b + c] for b, c in row_blocks(offs)])
+        ref, mag = FB.wgrad(V, V, offs), FB.wgrad(V, V, offs, absolute=True)
+        assert np.all(np.abs(dw.cpu().numpy() - ref) <= product_tol(ref, mag, R, "f32"))
+
+
 @pytest.mark.parametrize("R,n,k", [(1, 64, 128), (5, 256, 272), (500, 256, 384)])
 def test_gemm_without_offsets(R, n, k):
     rng = np.random.default_rng(R)
