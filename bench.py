@@ -53,12 +53,14 @@ def load_peaks():
 
 def kernel_sources_sha256() -> str:
     """sha256 of the sources the forward kernels are built from: every file of csrc in name
-    order except the backward-only ones (backward*.cuh), whose code is not part of the step."""
+    order except the backward-only ones (backward*.cuh) and the block-scaled 8-bit operators
+    (*fp8_block*), whose code is not part of the step."""
     import glob
     import hashlib
     h = hashlib.sha256()
     for f in sorted(glob.glob(os.path.join(ROOT, "fine_grained_mixture_moe_b200", "csrc", "*"))):
-        if os.path.basename(f).startswith("backward"):
+        name = os.path.basename(f)
+        if name.startswith("backward") or "fp8_block" in name:
             continue
         with open(f, "rb") as fh:
             h.update(fh.read())
