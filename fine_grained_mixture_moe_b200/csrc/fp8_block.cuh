@@ -7,8 +7,12 @@
 // Blocks run along a row (1 x 128), are square (128 x 128, weights), or run along the rows of one
 // expert (128 x 1, the operands of a weight gradient, whose inner dimension is the token).
 //
-// All of these kernels move each byte once and are bound by HBM: 16-byte loads per lane, the block
-// maximum by warp shuffles, the values held in registers between the maximum and the conversion.
+// All of these kernels move each byte once: 16-byte loads per lane, the block maximum by warp
+// shuffles, the values held in registers between the maximum and the conversion. The row-wise ones and
+// the weights are bound by HBM (rows 131,072 x 1,536 bf16: 90.4 us, 6.7 TB/s; weights 24 x 1,280 x 1,024
+// with the transposed copy: 21.3 us, 5.9 TB/s; SwiGLU forward 24,576 x 640: 20.2 us, 5.5 TB/s, backward
+// 131,072 x 768: 192 us, 6.3 TB/s), the token quantiser by instructions (from E4M3 rows 24,576 x 1,024:
+// 17 us; from bf16 ones 15.8 us).
 #pragma once
 #include <cuda_fp8.h>
 

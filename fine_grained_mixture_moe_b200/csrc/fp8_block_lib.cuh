@@ -93,20 +93,23 @@ moe_status_t launch_gemm_fp8_block(F8Gemm &p, const uint8_t *a, const uint8_t *b
   return launch_pdl(kern, dim3(2 * pairs), dim3(F8G_THREADS), smem, st, p);
 }
 
-// The form for few rows is chosen by its work in (16 weight rows x 16 rows x one K block) units, half a
-// group per expert taken as unfilled, against what the CTA-pair form takes at least (its start-up,
-// and K). Measured on both sides, few / pairs in us, rows on the first experts | spread over all:
-//   24 experts, n 1280, k 1024:  6 rows 4.3 / 10.4 | 4.3 / 10.4;   96: 8.2 / 10.4 | 10.7 / 14.7;
-//                                192: 12.3 / 10.7 | 13.7 / 14.9;   768: 35 / 11.5 | 39 / 15.3
-//   24 experts, n 1024, k 640:   192: 8.8 / 10.4 | 9.8 / 14.5;     384: 14.1 / 10.6 | 15.8 / 15.0
-//   256 experts, n 1024, k 1024: 32: 7.6 / 10.0 | 11.5 / 16.7;     64: 13.3 / 10.4 | 20.1 / 21.3
-//   8 experts, n 512, k 2048:    256: 10.2 / 13.5 | 11.1 / 13.3;   512: 16.6 / 13.7 | 17.8 / 13.5
-//   1 expert, n = k = 4096:      32: 15.9 / 19.7;                  64: 26.2 / 19.8
+// The form for few rows is chosen by its CTAs (16 weight rows x 16 rows; half a group of rows per expert
+// taken as unfilled) times the K blocks that each of a CTA's 8 warps does in turn, against the CTA-pair
+// form's start-up, K, and tiles of many experts. Measured on both sides, few / pairs in us, rows on the first experts | spread:
+//   24 experts, n 1280, k 1024:  6 rows 4.4 / 8.2 | 4.4 / 8.3;     48: 5.8 / 8.2 | 10.5 / 13.1;
+//                                96: 8.2 / 8.1 | 12.3 / 13.1;      192: 12.4 / 8.2 | 15.6 / 13.2
+//   24 experts, n 1024, k 640:   96: 6.0 / 6.9 | 9.3 / 10.6;       192: 8.7 / 7.0 | 11.5 / 10.8
+//   97 experts, n = k = 512:     48: 4.1 / 6.0 | 6.9 / 8.8;        96: 6.6 / 6.1 | 10.9 / 10.8
+//   256 experts, n = k = 1024:   32: 7.4 / 7.7 | 12.9 / 14.9;      64: 13.2 / 7.7 | 21.9 / 20.0
+//   8 experts, n 512, k 2048:    128: 9.7 / 10.4 | 10.1 / 10.9;    256: 10.1 / 10.8 | 11.7 / 10.9
+//   1 expert, n = k = 1024:      128: 7.0 / 8.2;                   256: 11.4 / 8.2
+//   1 expert, n = k = 4096:      16: 11.1 / 16.5;                  64: 28 / 17
 bool few_rows(long long rows, int E, int n, int k) {
   if (rows > 4096) return false;
   const int nkb = ceil_div(k, QB);
   const long long groups2 = 2 * rows / F8F_CHUNK + std::min<long long>(E, rows);  // twice the groups
-  return groups2 * (n / F8F_ROWS) * nkb <= 2 * (9000LL + 400LL * nkb);
+  return groups2 * (n / F8F_ROWS) * ceil_div(nkb, F8F_WARPS) <=
+         400 + 110LL * nkb + 75 * std::min<long long>(std::min(E, 24), rows);
 }
 
 moe_status_t launch_gemm_fp8_few(const F8Few &p, cudaStream_t st) {

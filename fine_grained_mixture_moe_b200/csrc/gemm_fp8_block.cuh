@@ -11,9 +11,10 @@
 // The scales are applied by the tensor core (kind::mxf8f6f4, block_scale): one E8M0 byte per row of
 // A and per row of B for each K = 32 instruction, read from TMEM. A TMEM word holds four bytes and the
 // instruction names one of them, so a word serves four blocks of 128, and the four instructions of a
-// block name the same byte. The fp32 accumulator of a tile stays in TMEM over the whole of
-// K and is read once; with the scales applied outside (a TMEM read and an fp32 multiply-add of every
-// element per block of K) the same tiles took 60 us instead of 27 on the Quartz gate|up product.
+// block name the same byte. The fp32 accumulator of a tile stays in TMEM over the whole of K and is
+// read once. Steps of the Quartz gate|up product (24,576 rows, n 1,280, k 1,024, six experts): scales
+// applied outside, a TMEM read and an fp32 multiply-add of every element per block of K, 59.6 us; in the
+// tensor core, one block per scale word, 42.0; four blocks per word, read once per CTA, 36.0.
 //
 // Clusters, stages and barriers are those of gemm_tc2.cuh: a tile of 256 x N (N = 16 .. 224) per CTA
 // pair, CTA r loads rows 128 r .. of the A tile and half of the N rows of B, the leader issues
@@ -22,8 +23,17 @@
 // wants them in all four), 4-11 store finished tiles, 12 loads, 13 issues.
 // TMEM: accumulator b in columns 256 b .. 256 b + N; the 32 columns from 256 b + 224 hold two of the
 // four scale buffers, each for four blocks of K (4 columns for 128 rows of A, up to 7 for N of B; 32
-// rows per column, one per lane). With one block per buffer the tensor core waited for its scales:
-// 42 us on the Quartz gate|up product.
+// rows per column, one per lane).
+//
+// Bound: the operands' way from L2. A stage is 60 KB per CTA for about 950 cycles of the tensor core;
+// three stages (all that shared memory holds) cycle in about 1,310, i.e. 46 bytes per cycle and SM
+// (13 TB/s in all), and the tensor pipe is 72% busy between tiles, 40% over the Quartz call (35.0 - 36.7
+// us, 1.8 PFLOP/s, start-up and last stores included), 2.2 PFLOP/s at 131,072 x 1,536 x 1,536 (278 -
+// 290 us). One block per stage (43 us), wider spacing of the tiles' K order (53 us: concurrent reads of
+// one line no longer meet), narrower tiles (47.5 us at 192), L2 prefetches and stores by the TMA unit
+// (37 us each) were slower. The weight gradient's fp32 output is its second bound: 61 - 84 us for the
+// Quartz gate|up gradient on six experts (32 blocks of K each, the rest zeros), 55.7 us with the
+// rows spread over all 24.
 #pragma once
 #include "fp8_block.cuh"
 #include "gemm_tc2.cuh"
