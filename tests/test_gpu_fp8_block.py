@@ -639,3 +639,58 @@ def test_large_addresses():
     ref, mag = FB.gemm(A, W, [0, 130, 300]), FB.gemm(A, W, [0, 130, 300], absolute=True)
     assert np.all(np.abs(out[-300:].cpu().numpy() - ref) <= product_tol(ref, mag, k, "f32"))
     assert not out[:-300].any()
+
+
+def _room(nbytes):
+    if torch.cuda.mem_get_info()[0] < 2 * nbytes:
+        pytest.skip("not enough device memory")
+
+
+def test_large_addresses_tokens_and_weight_gradient():
+    """Transposed codes of more than 2^31 bytes: only the last rows are not zero, so the last blocks and
+    the weight gradient are those of the last rows alone."""
+    R, k, n, tail = (1 << 20) + 40, 2064, 48, 168          # the last block holds 40 rows
+    _room(R * (3 * k + 4 * n))
+    x = torch.zeros((R, k), dtype=torch.bfloat16, device=DEV)
+    x[-tail:] = torch.randn((tail, k), device=DEV).to(torch.bfloat16)
+    dy = torch.zeros((R, n), device=DEV)
+    dy[-tail:] = torch.randn((tail, n), device=DEV)
+    offs = torch.tensor([0, R], dtype=torch.int32, device=DEV)
+    nb = B.moe_fp8_token_blocks(R, 1)
+    out = []
+    for t, C in ((dy, n), (x, k)):
+        q, s = u8(C, 128 * nb), u8(nb, C)
+        B.moe_quantize_fp8_tokens(t, None, R, C, offs, 1, q, s)
+        out += [q, s]
+    dw = torch.full((1, n, k), -7.0, device=DEV)
+    B.moe_wgrad_fp8_block(*out, R, offs, 1, n, k, dw)
+    check_device()
+    vals = []
+    for t, q, s in ((dy, out[0], out[1]), (x, out[2], out[3])):
+        rq, rs = FB.quantize_tokens(t[-tail:].float().cpu().numpy(), [0, tail])
+        assert np.array_equal(np8(q[:, -256:]), rq) and np.array_equal(np8(s[-2:]), rs)
+        assert not q[:, :-256].any() and (s[:-2] == 127).all()
+        vals.append(FB.values_tokens(rq, rs).T)
+    ref, mag = vals[0].T @ vals[1], np.abs(vals[0]).T @ np.abs(vals[1])
+    assert np.all(np.abs(dw[0].cpu().numpy() - ref) <= product_tol(ref, mag, tail, "f32"))
+
+
+def test_large_addresses_swiglu():
+    """More than 2^31 values: the last rows are what a call on them alone gives."""
+    R, f, tail = (1 << 20) + 24, 1024, 64
+    _room(R * f * 20)
+    gu = torch.randn((R, 2 * f), device=DEV, dtype=torch.bfloat16)
+    dh = torch.randn((R, f), device=DEV, dtype=torch.bfloat16)
+
+    def both(gu, dh):
+        R = gu.shape[0]
+        o = [torch.empty((R, f), dtype=torch.bfloat16, device=DEV), u8(R, f), u8(R, f // 128),
+             u8(R, 2 * f), u8(R, f // 64), torch.empty((R, 2 * f), dtype=torch.bfloat16, device=DEV),
+             u8(R, 2 * f), u8(R, f // 64)]
+        B.moe_swiglu_fp8_forward(gu, R, f, *o[:5])
+        B.moe_swiglu_fp8_backward(o[3], o[4], dh, R, f, *o[5:])
+        check_device()
+        return o
+    large = [t[-tail:].clone() for t in both(gu, dh)]
+    for a, b in zip(large, both(gu[-tail:].clone(), dh[-tail:].clone())):
+        assert torch.equal(a, b)
