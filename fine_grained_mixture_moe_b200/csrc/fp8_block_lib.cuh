@@ -71,6 +71,8 @@ moe_status_t launch_gemm_fp8_block(F8Gemm &p, const uint8_t *a, const uint8_t *b
   p.tn = f8g_tile_n(p.N);
   p.nt = ceil_div(p.N, p.tn);
   p.nt_mul = p.nt > 1 ? (unsigned)((1ull << 32) / p.nt) + 1u : 0u;
+  p.per = WGRAD ? ceil_div(p.M, 256) * p.nt : 1;
+  p.per_mul = p.per > 1 ? (unsigned)((1ull << 32) / p.per) + 1u : 0u;
   // two K blocks per copy when a row is whole K blocks (one box instead of two copies) and the tile
   // lists of E experts leave room for two such stages
   p.kpb = lda % QB == 0 && f8g_stages(p.E, p.tn, 2) >= 2 ? 2 : 1;

@@ -58,6 +58,8 @@ struct F8Gemm {
   int tn;                  // columns per tile, a multiple of 16 up to F8G_N
   int nt;                  // column tiles
   unsigned nt_mul;         // floor(2^32 / nt) + 1: x / nt = umulhi(x, nt_mul), or one less (nt > 1)
+  int per;                 // wgrad: tiles of a group, the same for all
+  unsigned per_mul;
   int out_f32;
   int stages, kpb;
 };
@@ -83,28 +85,48 @@ struct F8Tile {
   int kofs, nk;     // first K block and K blocks
 };
 
-// Tile counts per group scanned into prefix[0 .. E], and in start[0 .. E] the groups' first rows
-// (gemm) or first K blocks (wgrad).
+// x / d by its multiplier floor(2^32 / d) + 1 (any 32-bit x >= 0; d = 1 needs none).
+__device__ __forceinline__ int f8_div(int x, int d, unsigned mul) {
+  if (d == 1) return x;
+  const int q = (int)__umulhi((unsigned)x, mul);
+  return q * d > x ? q - 1 : q;
+}
+
+constexpr int F8G_SORT = 256;  // most groups that are put in order of K
+
+// start[0 .. E]: the groups' first rows (gemm) or first K blocks (wgrad). gemm: tile counts scanned into
+// prefix[0 .. E]. wgrad: every group has p.per tiles, and prefix[i] is the group at position i of the
+// list, longest K first (its rank, counted against every other group); with the rounds dealt to the
+// pairs in alternating direction the pairs' sums of K are nearly the same.
 template <bool WGRAD>
 __device__ __forceinline__ int f8_tile_prefix(const F8Gemm &p, int *prefix, int *start, int *tmp) {
-  const int nt = p.nt;
   for (int g = threadIdx.x; g <= p.E; g += blockDim.x) {
     const long long a = p.offsets ? expert_bound(p.offsets, g, p.rows) : g ? p.rows : 0;
     long long n = 0;
     if (g < p.E)
       n = max((p.offsets ? expert_bound(p.offsets, g + 1, p.rows) : p.rows) - a, 0ll);
     if (WGRAD) {
-      prefix[g] = ((p.M + 255) / 256) * nt;
       start[g] = (int)((n + QB - 1) / QB);
     } else {
-      prefix[g] = (int)((n + 255) / 256) * nt;
+      prefix[g] = (int)((n + 255) / 256) * p.nt;
       start[g] = (int)a;
     }
   }
   __syncthreads();
   if (WGRAD) {
+    for (int g = threadIdx.x; g < p.E; g += blockDim.x) {
+      int rank = g;
+      if (p.E <= F8G_SORT) {
+        rank = 0;
+        for (int h = 0; h < p.E; ++h) rank += start[h] > start[g] || (start[h] == start[g] && h < g);
+      }
+      prefix[rank] = g;
+    }
+    __syncthreads();
     const int all = block_excl_scan_inplace(start, p.E, tmp);
     if (threadIdx.x == 0) start[p.E] = all;
+    __syncthreads();
+    return p.E * p.per;
   }
   const int total = block_excl_scan_inplace(prefix, p.E, tmp);
   if (threadIdx.x == 0) prefix[p.E] = total;
@@ -112,33 +134,45 @@ __device__ __forceinline__ int f8_tile_prefix(const F8Gemm &p, int *prefix, int 
   return total;
 }
 
-// The group of a tile, and its K blocks (all that the issuing warp needs).
-__device__ __forceinline__ int f8_group(const F8Gemm &p, int tile, const int *prefix) {
+// The tile of a pair in round r (>= total: none in this round).
+template <bool WGRAD> __device__ __forceinline__ int f8_tile(int r, int pair, int npairs) {
+  return r * npairs + (WGRAD && (r & 1) ? npairs - 1 - pair : pair);
+}
+
+// The group of a tile and the tile's number in it.
+template <bool WGRAD>
+__device__ __forceinline__ int f8_group(const F8Gemm &p, int tile, const int *prefix, int *local) {
+  if (WGRAD) {
+    const int pos = f8_div(tile, p.per, p.per_mul);
+    *local = tile - pos * p.per;
+    return prefix[pos];
+  }
   int lo = 0, hi = p.E - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (prefix[mid] <= tile) lo = mid;
     else hi = mid - 1;
   }
+  *local = tile - prefix[lo];
   return lo;
 }
+// Its K blocks (all that the issuing warp needs); 0 past the last tile.
 template <bool WGRAD>
-__device__ __forceinline__ int f8_blocks(const F8Gemm &p, int tile, const int *prefix, const int *start) {
+__device__ __forceinline__ int f8_blocks(const F8Gemm &p, int tile, int total, const int *prefix,
+                                         const int *start) {
+  if (tile >= total) return 0;
   if (!WGRAD) return (p.K + QB - 1) / QB;
-  const int g = f8_group(p, tile, prefix);
+  int local;
+  const int g = f8_group<WGRAD>(p, tile, prefix, &local);
   return min(start[g + 1], p.K) - min(start[g], p.K);
 }
 
 template <bool WGRAD>
 __device__ __forceinline__ F8Tile f8_decode(const F8Gemm &p, int tile, const int *prefix, const int *start) {
   F8Tile t;
-  t.g = f8_group(p, tile, prefix);
-  const int local = tile - prefix[t.g];
-  int row = local;  // row and column of the tile: local / nt without a division
-  if (p.nt > 1) {
-    row = (int)__umulhi((unsigned)local, p.nt_mul);
-    if (row * p.nt > local) --row;
-  }
+  int local;
+  t.g = f8_group<WGRAD>(p, tile, prefix, &local);
+  const int row = f8_div(local, p.nt, p.nt_mul);
   t.m0 = row * 256;
   t.n0 = (local - row * p.nt) * p.tn;
   if (WGRAD) {
@@ -277,16 +311,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
     const int nkb = (p.K + QB - 1) / QB, nnb = (p.N + QB - 1) / QB;
     const bool word_a = !WGRAD && nkb % 4 == 0 && ((uintptr_t)p.a_scale & 3u) == 0;
     const bool word_b = !WGRAD && nkb % 4 == 0 && ((uintptr_t)p.b_scale & 3u) == 0;
-    int tile = pair, kb = 0, nk = 0;
+    int round = 0, kb = 0, nk = 0;
+    bool more = true;
     const uint8_t *src[3];
     bool on[3];
     auto enter = [&]() {  // the next tile that has K blocks
       F8Tile t;
-      for (; tile < total; tile += npairs) {
+      for (;; ++round) {
+        more = (long long)round * npairs < total;
+        if (!more) return;
+        const int tile = f8_tile<WGRAD>(round, pair, npairs);
+        if (tile >= total) continue;
         t = f8_decode<WGRAD>(p, tile, prefix, start);
         if (t.nk > 0) break;
       }
-      if (tile >= total) return;
       kb = 0;
       nk = t.nk;
       const int r = t.m0 + (int)rank * 128 + tid;
@@ -319,20 +357,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
       }
     };
     enter();
-    if (tile < total) fetch();
+    if (more) fetch();
     const uint32_t quarter = (uint32_t)(warp * 32) << 16;
     int unit = 0;
     uint32_t phase = 0;
-    while (tile < total) {
+    while (more) {
       uint32_t *mine = sf_words + (unit & 1) * 384;
 #pragma unroll
       for (int i = 0; i < 3; ++i) mine[128 * i + tid] = w[i][0] | w[i][1] << 8 | w[i][2] << 16 | w[i][3] << 24;
       kb += F8G_SF_K;
       if (kb >= nk) {
-        tile += npairs;
+        ++round;
         enter();
       }
-      if (tile < total) fetch();
+      if (more) fetch();
       // released by the tensor core, and the words of all four warps written; all four leave together
       if (!bar_all_128(f8_wait_warp(sfe_bar(unit), phase ^ 1u, abort_flag, limit, INFO_WAIT_MMA_EMPTY))) break;
       tc_fence_after();
@@ -354,7 +392,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
       uint32_t phase = 0;
       bool ok = true;
       uint32_t issued = 0, issued_parity = 0;  // bit s: stage s was filled, with that parity
-      for (int tile = pair; tile < total && ok; tile += npairs) {
+      for (int r = 0; (long long)r * npairs < total && ok; ++r) {
+        const int tile = f8_tile<WGRAD>(r, pair, npairs);
+        if (tile >= total) continue;
         const F8Tile t = f8_decode<WGRAD>(p, tile, prefix, start);
         // CTA 1's 128 rows may hold none of the group: never stored, so not loaded (gemm_tc2.cuh)
         const bool a1_void = t.m0 + 128 >= t.rows;
@@ -400,10 +440,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
       uint32_t phase = 0, acc_phase = 0, unit_phase = 0;
       bool ok = true, any = false;
       const uint64_t adesc0 = make_sdesc(smem_u32(base)), bdesc0 = make_sdesc(smem_u32(base) + a_stage);
-      int nk = pair < total ? f8_blocks<WGRAD>(p, pair, prefix, start) : 0;
-      for (int tile = pair; tile < total && ok; tile += npairs) {
+      int nk = f8_blocks<WGRAD>(p, pair, total, prefix, start);
+      for (int r = 0; (long long)r * npairs < total && ok; ++r) {
         const int left0 = nk;
-        nk = tile + npairs < total ? f8_blocks<WGRAD>(p, tile + npairs, prefix, start) : 0;
+        nk = f8_blocks<WGRAD>(p, f8_tile<WGRAD>(r + 1, pair, npairs), total, prefix, start);
         if (left0 == 0) continue;
         if (!mbar_try_wait(acce_bar(acc), acc_phase ^ 1u) &&
             !mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag, limit, INFO_WAIT_ACC_EMPTY)) {
@@ -462,7 +502,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
     const int ebytes = p.out_f32 ? 4 : 2, cpp = 128 / ebytes;  // columns per pass: 128 bytes of a row
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int tile = pair; tile < total; tile += npairs) {
+    for (int r = 0; (long long)r * npairs < total; ++r) {
+      const int tile = f8_tile<WGRAD>(r, pair, npairs);
+      if (tile >= total) continue;
       const F8Tile t = f8_decode<WGRAD>(p, tile, prefix, start);
       const int rbase = t.m0 + (int)rank * 128 + q * 32;
       const int nrows = min(32, t.rows - rbase), ncols = min(p.tn, p.N - t.n0);
