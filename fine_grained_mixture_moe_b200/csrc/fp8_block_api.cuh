@@ -117,13 +117,13 @@ moe_status_t moe_wgrad_fp8_block(const uint8_t *a_t, const uint8_t *a_scale, con
   MOE_F8B_WIDTH(n);
   MOE_F8B_WIDTH(k);
   if (token_blocks(rows, E) > (1ll << 24) - 1) return MOE_ERR_UNSUPPORTED;  // K coordinates
-  if ((long long)E * ceil_div(n, 256) * ceil_div(k, f8g_tile_n(k)) > MOE_F8B_TILES) return MOE_ERR_UNSUPPORTED;
+  if ((long long)E * ceil_div(n, 128) * ceil_div(k, 128) > MOE_F8B_TILES) return MOE_ERR_UNSUPPORTED;
   MOE_REQUIRE(aligned32(dw));
   cudaStream_t st = (cudaStream_t)stream;
   if (rows == 0)
     return cudaMemsetAsync(dw, 0, (size_t)E * n * k * sizeof(float), st) == cudaSuccess ? MOE_OK
                                                                                        : MOE_ERR_CUDA;
-  MOE_REQUIRE(aligned16(a_t) && a_scale && aligned16(b_t) && aligned4(b_scale) && aligned4(offsets));
+  MOE_REQUIRE(aligned16(a_t) && a_scale && aligned16(b_t) && b_scale && aligned4(offsets));
   F8Gemm p;
   std::memset(&p, 0, sizeof(p));
   p.offsets = offsets;

@@ -64,6 +64,15 @@ moe_status_t launch_quantize_tokens(const void *in, const uint8_t *in_scale, lon
 
 template <bool WGRAD>
 moe_status_t launch_gemm_fp8_block(F8Gemm &p, const uint8_t *a, const uint8_t *b, cudaStream_t st) {
+  // a tile is 256 rows by up to 224 columns: the weight gradient takes as rows the side that gives
+  // fewer tiles (1,280 x 1,024: 24 instead of 25, 896 x 1,024: 16 instead of 20)
+  if (WGRAD && ceil_div(p.N, 256) * ceil_div(p.M, f8g_tile_n(p.M)) <
+                   ceil_div(p.M, 256) * ceil_div(p.N, f8g_tile_n(p.N))) {
+    p.swap = 1;
+    std::swap(a, b);
+    std::swap(p.a_scale, p.b_scale);
+    std::swap(p.M, p.N);
+  }
   // one row of a (b) is K codes; wgrad: the token columns of every block
   const uint64_t lda = WGRAD ? (uint64_t)p.K * QB : (uint64_t)p.K;
   const uint64_t a_rows = WGRAD ? p.M : p.rows, b_rows = WGRAD ? (uint64_t)p.N : (uint64_t)p.E * p.N;

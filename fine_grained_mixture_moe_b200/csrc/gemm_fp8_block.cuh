@@ -31,9 +31,9 @@
 // us, 1.8 PFLOP/s, start-up and last stores included), 2.2 PFLOP/s at 131,072 x 1,536 x 1,536 (278 -
 // 290 us). One block per stage (43 us), wider spacing of the tiles' K order (53 us: concurrent reads of
 // one line no longer meet), narrower tiles (47.5 us at 192), L2 prefetches and stores by the TMA unit
-// (37 us each) were slower. The weight gradient's fp32 output is its second bound: 61 - 84 us for the
-// Quartz gate|up gradient on six experts (32 blocks of K each, the rest zeros), 55.7 us with the
-// rows spread over all 24.
+// (37 us each) were slower. The weight gradient's fp32 output is its second bound: 52 us for the Quartz
+// gate|up gradient on six experts (32 blocks of K each, the rest zeros; 60 with the other side as
+// rows, 25 tiles per expert instead of 24), 50 us with the rows spread over all 24 (56 in expert order).
 #pragma once
 #include "fp8_block.cuh"
 #include "gemm_tc2.cuh"
@@ -61,6 +61,7 @@ struct F8Gemm {
   int per;                 // wgrad: tiles of a group, the same for all
   unsigned per_mul;
   int out_f32;
+  int swap;                // wgrad: out is [E, N, M] (the operands changed places)
   int stages, kpb;
 };
 
@@ -518,7 +519,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
       // the two warps of a lane quarter take every other pass: 32 rows of the staging buffer, written
       // lane = row, read 8 lanes per row (whole 128-byte lines);
       // streaming stores, so that the operands stay in L2 (35.0 us instead of 36.0, Quartz gate|up)
-      if (nrows > 0)
+      if (WGRAD && p.swap) {
+        // a column of the tile is a row of out: 32 lanes write 128 bytes of it
+        float *col = (float *)p.out + ((size_t)t.g * p.N + t.n0) * p.M + rbase + lane;
+        if (nrows > 0)
+          for (int c = half * 32; c < ncols; c += 64) {
+            uint32_t r[32];
+            if (t.nk > 0) {
+              tmem_ld32(tb + c, r);
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) r[i] = 0u;
+            }
+            if (lane < nrows) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (c + i < ncols) __stcs(col + (size_t)(c + i) * p.M, __uint_as_float(r[i]));
+            }
+          }
+      } else if (nrows > 0)
         for (int c = half * cpp; c < ncols; c += 2 * cpp) {
           if (p.out_f32) {
             uint32_t r[32];

@@ -406,8 +406,8 @@ moe_status_t moe_gemm_fp8_block(const uint8_t *a, const uint8_t *a_scale, int64_
 
 /* Weight gradient: dw[e, c, i] = sum over the rows r of expert e of a[r, c] b[r, i], c < n, i < k
  * (a the product's upstream gradient, b its input), fp32 [E, n, k], 32-byte aligned; zeros for an
- * expert with no rows. a_t, a_scale: tokens layout of [rows, n]; b_t, b_scale: of [rows, k] (b_scale 4-byte
- * aligned), both made with these rows, offsets and E. */
+ * expert with no rows. a_t, a_scale: tokens layout of [rows, n]; b_t, b_scale: of [rows, k], both made with these
+ * rows, offsets and E. */
 moe_status_t moe_wgrad_fp8_block(const uint8_t *a_t, const uint8_t *a_scale, const uint8_t *b_t,
                                  const uint8_t *b_scale, int64_t rows, const int32_t *offsets,
                                  int32_t E, int32_t n, int32_t k, float *dw, void *stream);

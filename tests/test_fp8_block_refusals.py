@@ -89,7 +89,7 @@ def test_wgrad(lib):
         return f(v["a"], v["s"], v["b"], v["bs"], v["rows"], v["off"], v["E"], v["n"], v["k"],
                  v["dw"], None)
     assert call(rows=-4) == INVALID and call(n=24) == UNSUPPORTED and call(E=-1) == INVALID
-    for bad in (dict(a=None), dict(s=None), dict(b=P + 4), dict(bs=P + 1), dict(off=None),
+    for bad in (dict(a=None), dict(s=None), dict(b=P + 4), dict(bs=None), dict(off=None),
                 dict(dw=None), dict(dw=P + 8), dict(dw=P + 16)):
         assert call(**bad) == INVALID
 
