@@ -21,6 +21,7 @@
 namespace moe {
 
 constexpr int QB = 128;  // values per block
+constexpr long long INFO_OFFSETS_DECREASE = 4;  // detail code beside those of common.cuh
 
 // ------------------------------------------------------------------ the format
 // Scale byte of a block from the bits of its largest magnitude: amax = m 2^e with 1 <= m < 2 and
@@ -417,6 +418,12 @@ struct TokenBlock {
 __device__ __forceinline__ long long expert_bound(const int32_t *offsets, int e, long long rows) {
   return min(max((long long)__ldg(offsets + e), 0ll), rows);
 }
+// Offsets must not decrease (their clamped values then add up to at most `rows`): otherwise an error
+// is recorded and the caller does nothing.
+__device__ __forceinline__ bool offsets_decrease(bool bad) {
+  if (bad && threadIdx.x == 0) set_device_error(MOE_ERR_DEVICE_CHECK, INFO_OFFSETS_DECREASE);
+  return bad;
+}
 __device__ __forceinline__ bool find_token_block(const int32_t *offsets, int E, long long rows,
                                                  long long blk, TokenBlock *out) {
   const int lane = threadIdx.x & 31;
@@ -426,8 +433,9 @@ __device__ __forceinline__ bool find_token_block(const int32_t *offsets, int E, 
     int n = 0;
     if (e < E) {
       a = expert_bound(offsets, e, rows);
-      n = (int)max(expert_bound(offsets, e + 1, rows) - a, 0ll);
+      n = (int)(expert_bound(offsets, e + 1, rows) - a);
     }
+    if (offsets_decrease(__any_sync(0xffffffffu, n < 0))) return false;
     const int nb = (n + QB - 1) / QB;
     const int incl = warp_incl_scan(nb);
     const int total = __shfl_sync(0xffffffffu, incl, 31);

@@ -101,11 +101,13 @@ constexpr int F8G_SORT = 256;  // most groups that are put in order of K
 // pairs in alternating direction the pairs' sums of K are nearly the same.
 template <bool WGRAD>
 __device__ __forceinline__ int f8_tile_prefix(const F8Gemm &p, int *prefix, int *start, int *tmp) {
+  bool bad = false;
   for (int g = threadIdx.x; g <= p.E; g += blockDim.x) {
     const long long a = p.offsets ? expert_bound(p.offsets, g, p.rows) : g ? p.rows : 0;
     long long n = 0;
     if (g < p.E)
-      n = max((p.offsets ? expert_bound(p.offsets, g + 1, p.rows) : p.rows) - a, 0ll);
+      n = (p.offsets ? expert_bound(p.offsets, g + 1, p.rows) : p.rows) - a;
+    bad |= n < 0;
     if (WGRAD) {
       start[g] = (int)((n + QB - 1) / QB);
     } else {
@@ -113,7 +115,7 @@ __device__ __forceinline__ int f8_tile_prefix(const F8Gemm &p, int *prefix, int 
       start[g] = (int)a;
     }
   }
-  __syncthreads();
+  if (offsets_decrease(__syncthreads_or(bad))) return 0;
   if (WGRAD) {
     for (int g = threadIdx.x; g < p.E; g += blockDim.x) {
       int rank = g;
@@ -644,8 +646,13 @@ __device__ __forceinline__ bool find_few(const F8Few &p, int j, FewItem *it) {
     int off[5], sum = 0;
 #pragma unroll
     for (int i = 0; i < 5; ++i) off[i] = (int)expert_bound(p.offsets, min(e0 + 4 * lane + i, p.E), p.rows);
+    bool bad = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum += max((off[i + 1] - off[i] + F8F_CHUNK - 1) / F8F_CHUNK, 0);
+    for (int i = 0; i < 4; ++i) {
+      bad |= off[i + 1] < off[i];
+      sum += (off[i + 1] - off[i] + F8F_CHUNK - 1) / F8F_CHUNK;
+    }
+    if (offsets_decrease(__any_sync(0xffffffffu, bad))) return false;
     const int incl = warp_incl_scan(sum);
     const unsigned past = __ballot_sync(0xffffffffu, incl > j);
     if (past) {
@@ -655,7 +662,7 @@ __device__ __forceinline__ bool find_few(const F8Few &p, int j, FewItem *it) {
       for (int i = 0; i < 5; ++i) off[i] = __shfl_sync(0xffffffffu, off[i], src);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int n = max((off[i + 1] - off[i] + F8F_CHUNK - 1) / F8F_CHUNK, 0);
+        const int n = (off[i + 1] - off[i] + F8F_CHUNK - 1) / F8F_CHUNK;
         if (j >= 0 && j < n) {
           it->e = e0 + 4 * src + i;
           it->row = off[i] + j * F8F_CHUNK;

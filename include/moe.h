@@ -360,8 +360,9 @@ moe_status_t moe_quantize_fp8(const void *in, int32_t in_dtype, int64_t rows, in
  * For all of them: widths (cols, n, k; rows of a weight) are multiples of 16 up to 2^20,
  * 1 <= E <= 1024, rows < 2^31 - 4096 (more returns MOE_ERR_UNSUPPORTED), rows = 0 writes nothing
  * (moe_wgrad_fp8_block: zeros). offsets: [E+1] int32 on the device, non-decreasing, as
- * moe_permute returns them; entries are clamped to [0, rows], so no value of them reads or writes
- * out of bounds. n_rows: a device int32, the number of leading rows to process (offsets + E skips
+ * moe_permute returns them; entries are clamped to [0, rows]. Where the clamped values decrease, the
+ * device error MOE_ERR_DEVICE_CHECK (detail 4) is recorded and what the call writes is unspecified, but
+ * no value of them reads or writes out of bounds. n_rows: a device int32, the number of leading rows to process (offsets + E skips
  * the rows behind the last kept pair, which are neither read nor written), or NULL for all.
  * Pointers are 16-byte aligned; scale arrays need no alignment unless stated, offsets and n_rows
  * 4 bytes. Outputs must not overlap inputs. No workspace; safe to capture, to run on several
@@ -439,8 +440,8 @@ const char *moe_status_str(moe_status_t s);
  * (MOE_OK if no device-side fault was recorded). *info (may be NULL) receives a detail code:
  *   MOE_ERR_DEVICE_CHECK: 1 a sigmoid key that could not be resolved exactly; 2 an exact-sum
  *     expansion that ran out of terms; 3 a selected expert index outside [0, E) given to
- *     moe_route_backward; 100 + j an expert index outside [0, E) in slot j of moe_permute's
- *     topk_idx.
+ *     moe_route_backward; 4 offsets that decrease, given to a block-scaled operator; 100 + j an
+ *     expert index outside [0, E) in slot j of moe_permute's topk_idx.
  *   MOE_ERR_TIMEOUT: the bounded wait that ran out: 10 operands (MMA waiting for TMA), 11 a
  *     free stage (TMA waiting for the MMA), 12 a full accumulator, 13 a free accumulator, 14 the
  *     drain of copies still in flight, 15 the router's token rows, 16 the scatter's token rows,

@@ -330,10 +330,12 @@ def test_no_rows():
 
 @pytest.mark.parametrize("bad", [[0, 50, 20, 60], [0, 1000, 1000, 1000], [-5, 10, 2 ** 31 - 1, -1],
                                  [60, 40, 20, 0], [0, 60, 0, 60]])
-def test_offsets_out_of_range_stay_in_bounds(bad):
-    """Offsets that moe_permute never writes: clamped, so nothing outside the buffers is touched
-    (each buffer is the middle of a larger one whose ends must keep their fill)."""
-    R, E, n, k, pad = 60, 3, 64, 128, 1 << 16
+@pytest.mark.parametrize("R", [60, 5000])
+def test_offsets_out_of_range_stay_in_bounds(bad, R):
+    """Offsets that moe_permute never writes: clamped, or refused by the device where they decrease, so
+    nothing outside the buffers is touched (each buffer is the middle of a larger one whose ends must
+    keep their fill)."""
+    E, n, k, pad = 3, 64, 128, 1 << 16
     offs = torch.tensor(bad, dtype=torch.int32, device=DEV)
     nb = B.moe_fp8_token_blocks(R, E)
 
@@ -353,7 +355,9 @@ def test_offsets_out_of_range_stay_in_bounds(bad):
     qt, st = out(k * 128 * nb, torch.uint8), out(nb * k, torch.uint8)
     B.moe_quantize_fp8_tokens(q, s, R, k, offs, E, qt, st)
     B.moe_wgrad_fp8_block(qt, st, qt, st, R, offs, E, k, k, out(E * k * k, torch.float32))
-    check_device()
+    torch.cuda.synchronize()
+    clamped = np.clip(bad, 0, R)
+    assert B.moe_get_device_error() == ((6, 4) if (np.diff(clamped) < 0).any() else (0, 0))
     for o, numel in outer:
         assert (o[:pad] == 77).all() and (o[pad + numel:] == 77).all()
 
