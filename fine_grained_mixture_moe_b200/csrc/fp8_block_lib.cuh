@@ -92,7 +92,7 @@ moe_status_t launch_gemm_fp8_block(F8Gemm &p, const uint8_t *a, const uint8_t *b
                       : make_map(&p.ma, a, a_rows, lda, 128, 1) && make_map(&p.mb, b, b_rows, lda, bb, 1);
   if (!ok) return MOE_ERR_CUDA;
   const size_t smem = f8g_fixed_bytes(p.E) + (size_t)p.stages * f8g_stage_bytes(p.tn, p.kpb);
-  auto kern = gemm_fp8_block_kernel<WGRAD>;
+  auto kern = p.kpb == 2 ? gemm_fp8_block_kernel<WGRAD, 2> : gemm_fp8_block_kernel<WGRAD, 1>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return MOE_ERR_CUDA;
   const long long tiles = WGRAD ? (long long)p.E * ceil_div(p.M, 256) * ceil_div(p.N, p.tn)

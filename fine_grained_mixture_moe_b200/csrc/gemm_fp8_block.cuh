@@ -232,14 +232,14 @@ __device__ __forceinline__ bool f8_wait_warp(uint32_t bar, uint32_t parity, vola
   return __all_sync(0xffffffffu, ok);
 }
 
-template <bool WGRAD>
+template <bool WGRAD, int KPB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
     gemm_fp8_block_kernel(const __grid_constant__ F8Gemm p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int NST = p.stages, KPB = p.kpb;
+  const int NST = p.stages;
   const uint32_t b_bytes = (uint32_t)p.tn * 64;                     // this CTA's half of B, one K block
   const uint32_t a_stage = 16384u * KPB, stage_bytes = a_stage + b_bytes * KPB;
   // E4M3 operands, E8M0 scales, fp32 sums; the scales' byte (bits 4 and 29) is set per K block
@@ -441,6 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
       // one inlined barrier test, and the descriptors are kept as running values
       int stage = 0, acc = 0, unit = 0;
       uint32_t phase = 0, acc_phase = 0, unit_phase = 0;
+      uint32_t sf = sf_col(0);
       bool ok = true, any = false;
       const uint64_t adesc0 = make_sdesc(smem_u32(base)), bdesc0 = make_sdesc(smem_u32(base) + a_stage);
       int nk = f8_blocks<WGRAD>(p, pair, total, prefix, start);
@@ -454,37 +455,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
           break;
         }
         const uint32_t d = tmem_base + (uint32_t)(acc * 256);
-        uint32_t accumulate = 0;
         for (int kb = 0; kb < left0; kb += KPB) {
-          const bool first = kb % F8G_SF_K == 0;  // of a scale unit
-          if ((first && !mbar_try_wait(sff_bar(unit), unit_phase) &&
-               !mbar_wait(sff_bar(unit), unit_phase, abort_flag, limit, INFO_WAIT_TMA_FULL)) ||
-              (!mbar_try_wait(full_bar(stage), phase) &&
-               !mbar_wait(full_bar(stage), phase, abort_flag, limit, INFO_WAIT_TMA_FULL))) {
+          const uint32_t pos = (uint32_t)kb % F8G_SF_K;  // in the scale unit
+          if ((!mbar_try_wait(full_bar(stage), phase) &&
+               !mbar_wait(full_bar(stage), phase, abort_flag, limit, INFO_WAIT_TMA_FULL)) ||
+              (pos == 0 && !mbar_try_wait(sff_bar(unit), unit_phase) &&
+               !mbar_wait(sff_bar(unit), unit_phase, abort_flag, limit, INFO_WAIT_TMA_FULL))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t off = (uint64_t)(((uint32_t)stage * stage_bytes) >> 4);
-          uint64_t ad = adesc0 + off, bd = bdesc0 + off;
-          const uint32_t sf = sf_col(unit);
-          for (int j = 0; j < min(KPB, left0 - kb); ++j) {
-            const uint32_t byte = (uint32_t)(kb + j) % F8G_SF_K;
-            const uint32_t idesc = IDESC | byte << 4 | byte << 29;
+          const uint32_t off = ((uint32_t)stage * stage_bytes) >> 4;
+          const uint64_t ad = adesc0 + off, bd = bdesc0 + off;
+          const uint32_t idesc = IDESC | pos << 4 | pos << 29;
 #pragma unroll
-            for (int k32 = 0; k32 < 4; ++k32) {  // 32 bytes of K: two 16-byte units further
-              f8_mma(d, ad + 2 * k32, bd + 2 * k32, idesc, sf, sf + 4, accumulate);
-              accumulate = 1;
-            }
-            ad += 16384 >> 4;
-            bd += b_bytes >> 4;
+          for (int j = 0; j < KPB; ++j) {
+            if (j > 0 && kb + j >= left0) break;
+#pragma unroll
+            for (int k32 = 0; k32 < 4; ++k32)  // 32 bytes of K: two 16-byte units further
+              f8_mma(d, ad + (j * 1024 + 2 * k32), bd + (j * (b_bytes >> 4) + 2 * k32),
+                     idesc + j * (1u << 4 | 1u << 29), sf, sf + 4, j == 0 && k32 == 0 ? kb > 0 : 1u);
           }
           any = true;
           tc2_commit_both(empty_bar(stage));
           if (++stage == NST) { stage = 0; phase ^= 1u; }
-          if ((kb + KPB) % F8G_SF_K == 0 || kb + KPB >= left0) {
+          if (pos + KPB == F8G_SF_K || kb + KPB >= left0) {
             tc2_commit_both(sfe_bar(unit));
             if (++unit == F8G_SF_BUFS) { unit = 0; unit_phase ^= 1u; }
+            sf = sf_col(unit);
           }
         }
         if (!ok) break;
