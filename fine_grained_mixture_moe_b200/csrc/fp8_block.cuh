@@ -328,13 +328,16 @@ template <int V>
 __device__ __forceinline__ void tile_write(const uint32_t *tile, uint8_t *dst, size_t pitch, int cols,
                                            int rows) {
   const int g = threadIdx.x & 7;
-  for (int c = threadIdx.x >> 3; c < cols; c += F8T_THREADS / 8) {
-    if (16 * g >= rows) continue;
+  if (16 * g >= rows) return;
+  dst += (threadIdx.x >> 3) * pitch + 16 * g;
+#pragma unroll
+  for (int c = threadIdx.x >> 3; c < QB; c += F8T_THREADS / 8, dst += F8T_THREADS / 8 * pitch) {
+    if (c >= cols) break;
     const int key = tile_key<V>(c);
     uint4 v = *(const uint4 *)(tile + c * 32 + 4 * (g ^ (key >> 2)));
     if (key & 1) v = make_uint4(v.y, v.x, v.w, v.z);
     if (key & 2) v = make_uint4(v.z, v.w, v.x, v.y);
-    *(uint4 *)(dst + c * pitch + 16 * g) = v;
+    *(uint4 *)dst = v;
   }
 }
 
@@ -412,8 +415,8 @@ __global__ void __launch_bounds__(F8T_THREADS, sizeof(Tin) == 4 ? 2 : 4)
 // first row; block number `blk` in expert order. Every lane of a warp calls; returns false when
 // there are fewer blocks.
 struct TokenBlock {
-  long long row0;  // first row
-  int n;           // rows in it (1 .. 128)
+  int row0;  // first row
+  int n;     // rows in it (1 .. 128)
 };
 __device__ __forceinline__ long long expert_bound(const int32_t *offsets, int e, long long rows) {
   return min(max((long long)__ldg(offsets + e), 0ll), rows);
@@ -424,30 +427,27 @@ __device__ __forceinline__ bool offsets_decrease(bool bad) {
   if (bad && threadIdx.x == 0) set_device_error(MOE_ERR_DEVICE_CHECK, INFO_OFFSETS_DECREASE);
   return bad;
 }
-__device__ __forceinline__ bool find_token_block(const int32_t *offsets, int E, long long rows,
-                                                 long long blk, TokenBlock *out) {
+__device__ __forceinline__ bool find_token_block(const int32_t *offsets, int E, long long rows, int blk,
+                                                 TokenBlock *out) {
   const int lane = threadIdx.x & 31;
   for (int e0 = 0; e0 < E; e0 += 32) {
-    const int e = e0 + lane;
-    long long a = 0;
-    int n = 0;
-    if (e < E) {
-      a = expert_bound(offsets, e, rows);
-      n = (int)(expert_bound(offsets, e + 1, rows) - a);
+    int a = 0, n = 0;
+    if (e0 + lane < E) {
+      a = (int)expert_bound(offsets, e0 + lane, rows);
+      n = (int)expert_bound(offsets, e0 + lane + 1, rows) - a;
     }
     if (offsets_decrease(__any_sync(0xffffffffu, n < 0))) return false;
     const int nb = (n + QB - 1) / QB;
     const int incl = warp_incl_scan(nb);
-    const int total = __shfl_sync(0xffffffffu, incl, 31);
-    if (blk < total) {
-      const unsigned past = __ballot_sync(0xffffffffu, (long long)incl > blk);
+    const unsigned past = __ballot_sync(0xffffffffu, incl > blk);
+    if (past) {
       const int src = __ffs(past) - 1;
-      const int j = (int)blk - (__shfl_sync(0xffffffffu, incl, src) - __shfl_sync(0xffffffffu, nb, src));
-      out->row0 = __shfl_sync(0xffffffffu, a, src) + (long long)j * QB;
+      const int j = blk - __shfl_sync(0xffffffffu, incl - nb, src);
+      out->row0 = __shfl_sync(0xffffffffu, a, src) + j * QB;
       out->n = min(QB, __shfl_sync(0xffffffffu, n, src) - j * QB);
       return true;
     }
-    blk -= total;
+    blk -= __shfl_sync(0xffffffffu, incl, 31);
   }
   return false;
 }
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(F8T_THREADS, sizeof(Tin) == 4 ? 2 : 4)
                                  uint8_t *__restrict__ scale_t) {
   constexpr int V = 16 / sizeof(Tin), L = QB / V, A = F8T_THREADS / L, PASS = 32 / A;
   __shared__ __align__(16) uint32_t tile[QB * 32];
-  __shared__ __align__(16) uint32_t cmax[F8T_THREADS / 32][QB];
+  __shared__ __align__(16) float cmax[F8T_THREADS / 32][QB];
   const KernelStamp stamp(K_F8B_QUANT);
   griddep_wait();
   stamp.started();
@@ -476,16 +476,18 @@ __global__ void __launch_bounds__(F8T_THREADS, sizeof(Tin) == 4 ? 2 : 4)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Pack<Tin, V> p[PASS][4];
   float rs[PASS][4];  // the rows' own scales (8-bit input)
+  const size_t row = (size_t)tb.row0 + 4 * a0;  // this thread's first
+  const Tin *src = in + row * cols + col;
+  const uint8_t *src_scale = in_scale + row * ntile + ct;
+  const int left = col < cols ? tb.n - 4 * a0 : 0;
 #pragma unroll
   for (int s = 0; s < PASS; ++s)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = 4 * (a0 + s * A) + i;
       rs[s][i] = 1.0f;
-      if (r < tb.n && col < cols) {
-        p[s][i].load(in + (tb.row0 + r) * cols + col);
-        if (sizeof(Tin) == 1)
-          rs[s][i] = e8m0_value(__ldg(in_scale + (tb.row0 + r) * ntile + ct));
+      if (4 * A * s + i < left) {
+        p[s][i].load(src + (size_t)(4 * A * s + i) * cols);
+        if (sizeof(Tin) == 1) rs[s][i] = e8m0_value(__ldg(src_scale + (size_t)(4 * A * s + i) * ntile));
       } else {
         p[s][i].zero();
       }
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(F8T_THREADS, sizeof(Tin) == 4 ? 2 : 4)
   // column maxima, four columns (one word of codes to come) at a time
 #pragma unroll
   for (int j = 0; j < V / 4; ++j) {
-    uint32_t m[4] = {0, 0, 0, 0};
+    float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int s = 0; s < PASS; ++s)
 #pragma unroll
@@ -501,25 +503,25 @@ __global__ void __launch_bounds__(F8T_THREADS, sizeof(Tin) == 4 ? 2 : 4)
         float v[4];
         p[s][i].values4(j, v);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) m[x] = max(m[x], abs_bits(v[x] * rs[s][i]));
+        for (int x = 0; x < 4; ++x) m[x] = fmaxf(m[x], fabsf(v[x] * rs[s][i]));
       }
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
 #pragma unroll
       for (int o = L; o < 32; o <<= 1)  // lanes of the warp that hold the same columns
-        m[x] = max(m[x], __shfl_xor_sync(0xffffffffu, m[x], o));
+        m[x] = fmaxf(m[x], __shfl_xor_sync(0xffffffffu, m[x], o));
     }
-    if (lane < L) *(uint4 *)&cmax[warp][c0 + 4 * j] = make_uint4(m[0], m[1], m[2], m[3]);
+    if (lane < L) *(float4 *)&cmax[warp][c0 + 4 * j] = make_float4(m[0], m[1], m[2], m[3]);
   }
   __syncthreads();
   if (threadIdx.x < QB) {
-    uint32_t x = 0;
+    float x = 0.0f;
 #pragma unroll
-    for (int i = 0; i < F8T_THREADS / 32; ++i) x = max(x, cmax[i][threadIdx.x]);
-    const uint32_t b = e8m0_of_amax(x);
+    for (int i = 0; i < F8T_THREADS / 32; ++i) x = fmaxf(x, cmax[i][threadIdx.x]);
+    const uint32_t b = e8m0_of_amax(__float_as_uint(x));
     if (ct * QB + (int)threadIdx.x < cols)
       scale_t[(size_t)blk * cols + ct * QB + threadIdx.x] = (uint8_t)b;
-    cmax[0][threadIdx.x] = __float_as_uint(e8m0_inverse(b));
+    cmax[0][threadIdx.x] = e8m0_inverse(b);
   }
   __syncthreads();
 #pragma unroll

@@ -14,7 +14,8 @@
 // block name the same byte. The fp32 accumulator of a tile stays in TMEM over the whole of K and is
 // read once. Steps of the Quartz gate|up product (24,576 rows, n 1,280, k 1,024, six experts): scales
 // applied outside, a TMEM read and an fp32 multiply-add of every element per block of K, 59.6 us; in the
-// tensor core, one block per scale word, 42.0; four blocks per word, read once per CTA, 36.0.
+// tensor core, one block per scale word, 42.0; four blocks per word, read once per CTA, 36.0; streaming
+// stores and the issuing thread's loop unrolled over a stage, 35.0.
 //
 // Clusters, stages and barriers are those of gemm_tc2.cuh: a tile of 256 x N (N = 16 .. 224) per CTA
 // pair, CTA r loads rows 128 r .. of the A tile and half of the N rows of B, the leader issues
@@ -27,9 +28,9 @@
 //
 // Bound: the operands' way from L2. A stage is 60 KB per CTA for about 950 cycles of the tensor core;
 // three stages (all that shared memory holds) cycle in about 1,310, i.e. 46 bytes per cycle and SM
-// (13 TB/s in all), and the tensor pipe is 72% busy between tiles, 40% over the Quartz call (35.0 - 36.7
-// us, 1.8 PFLOP/s, start-up and last stores included), 2.2 PFLOP/s at 131,072 x 1,536 x 1,536 (278 -
-// 290 us). One block per stage (43 us), wider spacing of the tiles' K order (53 us: concurrent reads of
+// (13 TB/s in all), and the tensor pipe is 72% busy between tiles, 40% over the Quartz call (35.0 - 35.4
+// us, 1.8 PFLOP/s, start-up and last stores included), 2.3 PFLOP/s at 131,072 x 1,536 x 1,536 (265 -
+// 273 us; 316 - 325 at the clocks of the power cap, 1,300 MHz, when repeated for seconds). One block per stage (43 us), wider spacing of the tiles' K order (53 us: concurrent reads of
 // one line no longer meet), narrower tiles (47.5 us at 192), L2 prefetches and stores by the TMA unit
 // (37 us each) were slower. The weight gradient's fp32 output is its second bound: 52 us for the Quartz
 // gate|up gradient on six experts (32 blocks of K each, the rest zeros; 60 with the other side as
