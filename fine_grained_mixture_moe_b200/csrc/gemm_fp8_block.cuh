@@ -438,8 +438,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
   } else if (warp == 13) {
     // ------------------------------------------------------------ MMA issuer (leader only)
     if (rank == 0 && lane == 0) {
-      // the tensor core drains its queue in a few hundred cycles: between two stages this thread does
-      // one inlined barrier test, and the descriptors are kept as running values
+      // the tensor core drains its queue in a few hundred cycles, so every cycle of this thread between
+      // two stages counts (300 more per tile cost 5%): inlined barrier tests, a stage's instructions
+      // unrolled, the next tile's K looked up ahead
       int stage = 0, acc = 0, unit = 0;
       uint32_t phase = 0, acc_phase = 0, unit_phase = 0;
       uint32_t sf = sf_col(0);
@@ -517,9 +518,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
       unsigned char *out = (unsigned char *)p.out + ((size_t)(t.row0 + rbase) * p.N + t.n0) * ebytes;
       const size_t pitch = (size_t)p.N * ebytes;
-      // the two warps of a lane quarter take every other pass: 32 rows of the staging buffer, written
-      // lane = row, read 8 lanes per row (whole 128-byte lines);
-      // streaming stores, so that the operands stay in L2 (35.0 us instead of 36.0, Quartz gate|up)
+      // The two warps of a lane quarter take every other pass: 32 rows of the staging buffer, written
+      // lane = row, read 8 lanes per row (whole 128-byte lines). Streaming stores, so that the operands
+      // stay in L2 (35.0 us instead of 36.0, Quartz gate|up).
       if (WGRAD && p.swap) {
         // a column of the tile is a row of out: 32 lanes write 128 bytes of it
         float *col = (float *)p.out + ((size_t)t.g * p.N + t.n0) * p.M + rbase + lane;
@@ -724,7 +725,11 @@ __device__ __forceinline__ void few_chunk(const F8Few &p, int e, long long row, 
         mma_e4m3(c, wa[0][h].z, wa[1][h].z, wa[0][h].w, wa[1][h].w, xb[i][h].z, xb[i][h].w);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(c[j], sx[i][j & 1] * sw, acc[i][j]);
+      for (int j = 0; j < 4; ++j) {
+        // the smaller scale first: their product alone may leave the range where the sum does not
+        const float s = sx[i][j & 1];
+        acc[i][j] = fmaf(c[j] * (s < sw ? s : sw), s < sw ? sw : s, acc[i][j]);
+      }
     }
   }
   // red[warp][token][16 weight rows]

@@ -258,6 +258,30 @@ def test_rows_before_the_first_expert(R, E, n, k):
         assert np.all(np.abs(dw.cpu().numpy() - ref) <= product_tol(ref, mag, R, "f32"))
 
 
+@pytest.mark.parametrize("R,n", [(3, 64), (16, 64), (600, 256)])
+@pytest.mark.parametrize("idle", [(254, 254), (1, 1), (254, 1), (200, 200)])
+@pytest.mark.parametrize("pair", [(240, 14), (14, 240), (254, 1), (1, 254), (127, 127), (20, 220)])
+def test_gemm_scale_bytes_at_both_ends(R, n, idle, pair):
+    """Two scales whose product leaves the range of fp32 on a block whose sum is zero, and ones that
+    make up for each other: the result is the sum, in the form for few rows and in the other."""
+    rng = np.random.default_rng(R + sum(idle) + sum(pair))
+    k = 256
+    q, w = (rng.integers(0, 0x7F, (m, k)).astype(np.uint8) for m in (R, n))
+    q[:, 0:128:2] = 0                                    # block 0: no code meets a code
+    w[:, 1:128:2] = 0
+    w = w[None]
+    s = np.tile(np.array([idle[0], pair[0]], np.uint8), (R, 1))
+    ws = np.tile(np.array([idle[1], pair[1]], np.uint8), (1, -(-n // 128), 1))
+    out = torch.empty(R, n, device=DEV)
+    d = [torch.from_numpy(a).to(DEV) for a in (q, s, w, ws)]
+    B.moe_gemm_fp8_block(d[0], d[1], R, None, 1, n, k, d[2], d[3], out)
+    check_device()
+    offs = np.array([0, R])
+    A, W = FB.values_rows(q, s)[:, 128:], FB.values_weight(w, ws)[:, :, 128:]
+    ref, mag = FB.gemm(A, W, offs), FB.gemm(A, W, offs, absolute=True)
+    assert np.all(np.abs(out.cpu().numpy() - ref) <= product_tol(ref, mag, k, "f32"))
+
+
 @pytest.mark.parametrize("R,n,k", [(1, 64, 128), (5, 256, 272), (500, 256, 384)])
 def test_gemm_without_offsets(R, n, k):
     rng = np.random.default_rng(R)
