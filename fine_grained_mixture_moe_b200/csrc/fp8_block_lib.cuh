@@ -87,14 +87,16 @@ moe_status_t launch_gemm_fp8_block(F8Gemm &p, const uint8_t *a, const uint8_t *b
   p.kpb = lda % QB == 0 && f8g_stages(p.E, p.tn, 2) >= 2 ? 2 : 1;
   p.stages = f8g_stages(p.E, p.tn, p.kpb);
   const uint32_t bb = p.tn / 2;
+  auto kern = p.kpb == 2 ? gemm_fp8_block_kernel<WGRAD, 2> : gemm_fp8_block_kernel<WGRAD, 1>;
+  // Before the maps: it binds the device's context to a thread that has made no call yet, which the
+  // driver's encoder asks for.
+  const size_t smem = f8g_fixed_bytes(p.E) + (size_t)p.stages * f8g_stage_bytes(p.tn, p.kpb);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return MOE_ERR_CUDA;
   const bool ok = p.kpb == 2
                       ? make_map3_u8(&p.ma, a, a_rows, lda, 128) && make_map3_u8(&p.mb, b, b_rows, lda, bb)
                       : make_map(&p.ma, a, a_rows, lda, 128, 1) && make_map(&p.mb, b, b_rows, lda, bb, 1);
   if (!ok) return MOE_ERR_CUDA;
-  const size_t smem = f8g_fixed_bytes(p.E) + (size_t)p.stages * f8g_stage_bytes(p.tn, p.kpb);
-  auto kern = p.kpb == 2 ? gemm_fp8_block_kernel<WGRAD, 2> : gemm_fp8_block_kernel<WGRAD, 1>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return MOE_ERR_CUDA;
   const long long tiles = WGRAD ? (long long)p.E * ceil_div(p.M, 256) * ceil_div(p.N, p.tn)
                                 : (ceil_div(p.rows, 256) + std::min<long long>(p.E, p.rows)) *
                                       ceil_div(p.N, p.tn);

@@ -645,6 +645,38 @@ def test_reproducible_streams_and_graphs():
     assert not torch.equal(got[0], first[0])
 
 
+@pytest.mark.parametrize("call", ["gemm", "wgrad"])
+def test_first_call_of_a_thread(call):
+    """A thread whose first use of the GPU is a product (the driver's context is not yet bound to it)."""
+    import threading
+    R, n, k = 8192, 128, 256
+    rng = np.random.default_rng(5)
+    offs = np.array([0, R], np.int32)
+    q, s = FB.quantize_rows(rng.standard_normal((R, k)))
+    w, ws = FB.quantize_weight(rng.standard_normal((1, n, k)))
+    xq, xs = FB.quantize_tokens(rng.standard_normal((R, k)), offs)
+    d = [torch.from_numpy(a).to(DEV) for a in (q, s, offs, w, ws, xq, xs)]
+    outs = [torch.empty((R, n) if call == "gemm" else (k, k), device=DEV) for _ in range(2)]
+    st = torch.cuda.current_stream().cuda_stream
+    status = []
+
+    def run(out):
+        p = [t.data_ptr() for t in d]
+        if call == "gemm":
+            status.append(B.load().moe_gemm_fp8_block(p[0], p[1], R, p[2], 1, n, k, p[3], p[4],
+                                                      out.data_ptr(), 0, st))
+        else:
+            status.append(B.load().moe_wgrad_fp8_block(p[5], p[6], p[5], p[6], R, p[2], 1, k, k,
+                                                       out.data_ptr(), st))
+    run(outs[0])
+    t = threading.Thread(target=run, args=(outs[1],))
+    t.start()
+    t.join()
+    check_device()
+    assert status == [0, 0]
+    assert torch.equal(outs[0], outs[1])
+
+
 def test_large_addresses():
     """Codes of more than 2^31 bytes: the last rows are quantised and multiplied like the first."""
     R, k, n = (1 << 20) + 40, 2064, 48
