@@ -89,9 +89,9 @@ moe_status_t launch_gemm_fp8_block(F8Gemm &p, const uint8_t *a, const uint8_t *b
   const uint32_t bb = p.tn / 2;
   auto kern = p.kpb == 2 ? gemm_fp8_block_kernel<WGRAD, 2> : gemm_fp8_block_kernel<WGRAD, 1>;
   // Before the maps: it binds the device's context to a thread that has made no call yet, which the
-  // driver's encoder asks for.
-  const size_t smem = f8g_fixed_bytes(p.E) + (size_t)p.stages * f8g_stage_bytes(p.tn, p.kpb);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  // driver's encoder asks for. One value for every call: a call's own size could be lowered by another
+  // thread's before the launch.
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F8G_MAX_SMEM) != cudaSuccess)
     return MOE_ERR_CUDA;
   const bool ok = p.kpb == 2
                       ? make_map3_u8(&p.ma, a, a_rows, lda, 128) && make_map3_u8(&p.mb, b, b_rows, lda, bb)
@@ -101,6 +101,7 @@ moe_status_t launch_gemm_fp8_block(F8Gemm &p, const uint8_t *a, const uint8_t *b
                                 : (ceil_div(p.rows, 256) + std::min<long long>(p.E, p.rows)) *
                                       ceil_div(p.N, p.tn);
   const int pairs = (int)std::min<long long>(num_sms() / 2, tiles);
+  const size_t smem = f8g_fixed_bytes(p.E) + (size_t)p.stages * f8g_stage_bytes(p.tn, p.kpb);
   const int kind = WGRAD ? K_F8B_WGRAD : K_F8B_GEMM;
   ProfScope ps(kind, st);
   return launch_pdl(kern, dim3(2 * pairs), dim3(F8G_THREADS), smem, st, p);

@@ -75,8 +75,9 @@ inline size_t f8g_fixed_bytes(int E) {
   return 1024 + (size_t)F8G_STG + 256 + F8G_SF_BYTES + (size_t)(2 * E + 2 + F8G_THREADS / 32 + 1) * sizeof(int);
 }
 inline int f8g_stage_bytes(int tn, int kpb) { return (16384 + tn * 64) * kpb; }
+constexpr int F8G_MAX_SMEM = 227 * 1024;
 inline int f8g_stages(int E, int tn, int kpb) {
-  const long long n = (227LL * 1024 - (long long)f8g_fixed_bytes(E)) / f8g_stage_bytes(tn, kpb);
+  const long long n = ((long long)F8G_MAX_SMEM - (long long)f8g_fixed_bytes(E)) / f8g_stage_bytes(tn, kpb);
   return n > 8 / kpb ? 8 / kpb : (int)n;
 }
 

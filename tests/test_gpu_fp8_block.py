@@ -677,6 +677,40 @@ def test_first_call_of_a_thread(call):
     assert torch.equal(outs[0], outs[1])
 
 
+def test_several_threads():
+    """Calls of one kernel with different numbers of experts (and so different shared memory) from
+    several threads at once, each on its own stream."""
+    from concurrent.futures import ThreadPoolExecutor
+    n = k = 128
+    calls = 400
+
+    def case(E):
+        rng = np.random.default_rng(E)
+        R = 8192
+        offs = splits("even", R, E, rng)
+        q, s = FB.quantize_rows(rng.standard_normal((R, k)))
+        w, ws = FB.quantize_weight(rng.standard_normal((E, n, k)))
+        d = [torch.from_numpy(a).to(DEV) for a in (q, s, offs, w, ws)]
+        return R, E, d, torch.empty(R, n, device=DEV), torch.empty(R, n, device=DEV)
+
+    def run(c):
+        R, E, d, first, out = c
+        st = torch.cuda.Stream()
+        for i in range(calls):
+            B.moe_gemm_fp8_block(d[0], d[1], R, d[2], E, n, k, d[3], d[4], out, stream=st)
+        st.synchronize()
+    cases = [case(E) for E in (1, 1024, 64, 512)]
+    for R, E, d, first, _ in cases:
+        B.moe_gemm_fp8_block(d[0], d[1], R, d[2], E, n, k, d[3], d[4], first)
+    torch.cuda.synchronize()
+    with ThreadPoolExecutor(len(cases)) as pool:
+        for f in [pool.submit(run, c) for c in cases]:
+            f.result()
+    check_device()
+    for R, E, d, first, out in cases:
+        assert torch.equal(first, out)
+
+
 def test_large_addresses():
     """Codes of more than 2^31 bytes: the last rows are quantised and multiplied like the first."""
     R, k, n = (1 << 20) + 40, 2064, 48
