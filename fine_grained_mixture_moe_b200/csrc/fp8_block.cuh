@@ -667,8 +667,8 @@ __global__ void __launch_bounds__(256, 4)
         for (int j = 0; j < 2; ++j) {
           const float s = sigmoid_f(gg[j]), gs = gg[j] * s;
           du[x][i + j] = d[i + j] * gs;
-          // s (1 + g (1 - s)) = s + g s (1 - s)
-          dg[x][i + j] = d[i + j] * uu[j] * fmaf(gs, 1.0f - s, s);
+          // s (1 + g (1 - s)) = s + g s (1 - s), at most 1.1: no overflow before the last factor
+          dg[x][i + j] = d[i + j] * fmaf(gs, 1.0f - s, s) * uu[j];
           hv[i + j] = gs * uu[j];
         }
       }

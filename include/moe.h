@@ -414,10 +414,10 @@ moe_status_t moe_wgrad_fp8_block(const uint8_t *a_t, const uint8_t *a_scale, con
                                  int32_t E, int32_t n, int32_t k, float *dw, void *stream);
 
 /* SwiGLU that keeps its input in 8 bits: gu [rows, 2 ffn] = [gate | up] (bf16 or fp32),
- * h = silu(gate) * up in fp32; h as bf16 to `h`, and / or in the rows layout [rows, ffn] to h_q,
- * h_scale (the down product's operand); the checkpoint, gu in the rows layout [rows, 2 ffn], to
- * gu_q, gu_scale. Each of the three outputs may be NULL, not all. ffn a multiple of 128 (no block
- * spans gate and up; otherwise MOE_ERR_UNSUPPORTED). */
+ * h = silu(gate) * up in fp32 (a sigmoid below 2^-126 counts as 0); h as bf16 to `h`, and / or in
+ * the rows layout [rows, ffn] to h_q, h_scale (the down product's operand); the checkpoint, gu in the
+ * rows layout [rows, 2 ffn], to gu_q, gu_scale. Each of the three outputs may be NULL, not all. ffn a
+ * multiple of 128 (no block spans gate and up; otherwise MOE_ERR_UNSUPPORTED). */
 moe_status_t moe_swiglu_fp8_forward(const void *gu, int32_t in_dtype, int64_t rows, int32_t ffn,
                                     const int32_t *n_rows, void *h, uint8_t *h_q, uint8_t *h_scale,
                                     uint8_t *gu_q, uint8_t *gu_scale, void *stream);

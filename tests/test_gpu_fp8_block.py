@@ -462,6 +462,22 @@ def test_swiglu_backward(dtype, R, f):
     check_codes(np8(dq), np8(ds), ref, err)
 
 
+def test_swiglu_backward_of_large_factors():
+    """dh and up whose product leaves the range of fp32 beside a slope that is zero."""
+    f = 128
+    gu = np.zeros((2, 2 * f), np.float32)
+    gu[:, :f] = [[-2.0 ** 13], [-2.0 ** 20]]
+    gu[:, f:] = 2.0 ** 100
+    gq, gs = FB.quantize_rows(gu)
+    d = [torch.from_numpy(a).to(DEV) for a in (gq, gs)]
+    dh = torch.full((2, f), 2.0 ** 60, device=DEV)
+    dgu = torch.full((2, 2 * f), -7.0, dtype=torch.bfloat16, device=DEV)
+    dq, ds = u8(2, 2 * f), u8(2, 2)
+    B.moe_swiglu_fp8_backward(d[0], d[1], dh, 2, f, dgu, dq, ds)
+    check_device()
+    assert (dgu == 0).all() and (np8(dq) & 0x7F == 0).all() and (np8(ds) == 127).all()
+
+
 @pytest.mark.parametrize("n", [0, 3, 29, 50])
 def test_swiglu_rows_behind_the_counter_are_left(n):
     R, f = 29, 256
