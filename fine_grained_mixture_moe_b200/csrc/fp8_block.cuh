@@ -427,6 +427,15 @@ __device__ __forceinline__ bool offsets_decrease(bool bad) {
   if (bad && threadIdx.x == 0) set_device_error(MOE_ERR_DEVICE_CHECK, INFO_OFFSETS_DECREASE);
   return bad;
 }
+// All offsets, by one warp: a CTA's search ends at its block or group of rows, so that the experts behind
+// the last one's are seen by none. The grid's last CTA calls this when its own work is done (within the
+// search it cost registers that the quantiser needs: 17.8 -> 20.4 us).
+__device__ __forceinline__ void check_offsets(const int32_t *offsets, int E, long long rows) {
+  bool bad = false;
+  for (int e = threadIdx.x & 31; e < E; e += 32)
+    bad |= expert_bound(offsets, e + 1, rows) < expert_bound(offsets, e, rows);
+  offsets_decrease(__any_sync(0xffffffffu, bad));
+}
 __device__ __forceinline__ bool find_token_block(const int32_t *offsets, int E, long long rows, int blk,
                                                  TokenBlock *out) {
   const int lane = threadIdx.x & 31;
@@ -543,6 +552,7 @@ __global__ void __launch_bounds__(F8T_THREADS, sizeof(Tin) == 4 ? 2 : 4)
   __syncthreads();
   tile_write<V>(tile, q_t + (size_t)ct * QB * pitch + (size_t)blk * QB, pitch, min(QB, cols - ct * QB),
                 QB);
+  if (blockIdx.x == gridDim.x - 1 && threadIdx.x < 32) check_offsets(offsets, E, rows);
 }
 
 // ------------------------------------------------------------------ SwiGLU with a checkpoint

@@ -760,6 +760,8 @@ __global__ void __launch_bounds__(32 * F8F_WARPS, 4) gemm_fp8_few_kernel(const _
   if (!find_few(p, blockIdx.y, &it)) return;
   if (it.cnt <= 8) few_chunk<1>(p, it.e, it.row, it.cnt, blockIdx.x * F8F_ROWS, red);
   else few_chunk<F8F_CHUNK / 8>(p, it.e, it.row, it.cnt, blockIdx.x * F8F_ROWS, red);
+  if (p.offsets && blockIdx.x == 0 && blockIdx.y == gridDim.y - 1 && threadIdx.x < 32)
+    check_offsets(p.offsets, p.E, p.rows);
 }
 
 }  // namespace moe

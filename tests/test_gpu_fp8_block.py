@@ -386,6 +386,29 @@ def test_offsets_out_of_range_stay_in_bounds(bad, R):
         assert (o[:pad] == 77).all() and (o[pad + numel:] == 77).all()
 
 
+def test_offsets_that_decrease_behind_the_last_block():
+    """One row for each of the first experts, so that every block and group of rows is found among them,
+    and offsets that decrease much later."""
+    R, E, n, k = 64, 1024, 16, 128
+    offs = np.minimum(np.arange(E + 1), R).astype(np.int32)
+    nb = B.moe_fp8_token_blocks(R, E)
+    assert nb == R
+    q, s, w, ws = u8(R, k, fill=0x38), u8(R, 1, fill=127), u8(E, n, k, fill=0x38), u8(E, 1, 1, fill=127)
+    qt, st = u8(k, 128 * nb), u8(nb, k)
+    out = torch.empty(R, n, device=DEV)
+    for at in (None, 40, 129, 700, 1023):
+        o = offs.copy()
+        if at is not None:
+            o[at] = 7
+        o = torch.from_numpy(o).to(DEV)
+        for call in (lambda: B.moe_gemm_fp8_block(q, s, R, o, E, n, k, w, ws, out),
+                     lambda: B.moe_quantize_fp8_tokens(q, s, R, k, o, E, qt, st)):
+            call()
+            torch.cuda.synchronize()
+            assert B.moe_get_device_error() == ((0, 0) if at is None else (6, 4))
+    assert B.moe_get_device_error() == (0, 0)
+
+
 # ------------------------------------------------------------------ SwiGLU
 def check_codes(q, s, ref, err):
     """Codes and bytes of values known to within `err` of `ref`: the byte is the scale of an amax
