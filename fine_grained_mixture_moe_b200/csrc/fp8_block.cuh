@@ -16,6 +16,8 @@
 #pragma once
 #include <cuda_fp8.h>
 
+#include <cfloat>
+
 #include "common.cuh"
 
 namespace moe {
@@ -31,7 +33,7 @@ __device__ __forceinline__ uint32_t e8m0_of_amax(uint32_t amax_bits) {
   const int b = (int)((amax_bits + 0x1FFFFFu) >> 23) - 8;
   return (uint32_t)max(b, 1);
 }
-// 2^(b - 127) and its reciprocal, both normal for the bytes 1 .. 248 that e8m0_of_amax returns
+// 2^(b - 127), and its reciprocal, a normal number for the bytes 1 .. 247 of finite fp32 values
 __device__ __forceinline__ float e8m0_value(uint32_t b) { return __uint_as_float(b << 23); }
 __device__ __forceinline__ float e8m0_inverse(uint32_t b) {
   return __uint_as_float((254u - b) << 23);
@@ -306,11 +308,11 @@ __device__ __forceinline__ void transpose4(const uint32_t (&in)[4], uint32_t (&o
   out[2] = __byte_perm(c, d, 0x5410);
   out[3] = __byte_perm(c, d, 0x7632);
 }
-// w[i][j]: codes of row 4a + i, columns col + 4j .. col + 4j + 3.
-template <int V>
-__device__ __forceinline__ void tile_put(uint32_t *tile, int a, int col, const uint32_t (&w)[4][V / 4]) {
+// w[i][j]: codes of row 4a + i, columns col + 4j .. col + 4j + 3 (W columns).
+template <int V, int W = V>
+__device__ __forceinline__ void tile_put(uint32_t *tile, int a, int col, const uint32_t (&w)[4][W / 4]) {
 #pragma unroll
-  for (int j = 0; j < V / 4; ++j) {
+  for (int j = 0; j < W / 4; ++j) {
     const uint32_t in[4] = {w[0][j], w[1][j], w[2][j], w[3][j]};
     uint32_t out[4];
     transpose4(in, out);
@@ -461,6 +463,49 @@ __device__ __forceinline__ bool find_token_block(const int32_t *offsets, int E, 
   return false;
 }
 
+// A tile of codes with values past fp32's largest (2^-135 .. 448 2^127 are possible): its column bytes,
+// and its codes into shared memory. 2^-8 of a value is exact in fp32, its subnormals included, and of an
+// amax that small the byte is the exponent of the largest (that it is one of fp32's subnormals below
+// 2^-118 makes no difference, as byte 1 is the least). A code times 2^(row's byte - column's byte) is one
+// exact product: a factor past 2^127 meets only zero codes, and what one below 2^-126 (taken as 0) meets
+// is far below half the least code. Rows of finite fp32 values have at most a few such values (above
+// 1.9375 2^127 they round up to 2^128), so this reads its inputs again and is not made fast; a call of
+// its own after the ordinary encoding, so that other tiles lose little (17.8 -> 18.2 us; 18.9 as a branch
+// before the encoding, 21 inlined there).
+__device__ __noinline__ void put_loud_tile(const uint8_t *src, const uint8_t *src_scale, int cols, int ntile,
+                                           int n, int left_cols, uint32_t *tile, uint8_t *col_byte,
+                                           uint8_t *scale_t) {
+  const int c = threadIdx.x;
+  if (c < QB) {
+    uint32_t b = 127;
+    if (c < left_cols) {
+      float m = 0.0f;
+      for (int r = 0; r < n; ++r) {
+        const float v = e4m3x2_values(src[(size_t)r * cols + c]).x;
+        m = fmaxf(m, fabsf(v * (e8m0_value(src_scale[(size_t)r * ntile]) * 0x1p-8f)));
+      }
+      if (m > 0.0f) b = max((__float_as_uint(m) + 0x1FFFFFu) >> 23, 1u);
+      scale_t[c] = (uint8_t)b;
+    }
+    col_byte[c] = (uint8_t)b;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < QB / 4 * (QB / 4); i += F8T_THREADS) {  // words of 4 rows by 4 columns
+    const int a = i / (QB / 4), c0 = i % (QB / 4) * 4;
+    uint32_t w[4][1] = {};
+    for (int r = 4 * a; r < min(n, 4 * a + 4) && c0 < left_cols; ++r) {
+      const uint32_t codes = *(const uint32_t *)(src + (size_t)r * cols + c0);
+      const int row = src_scale[(size_t)r * ntile];
+      const float2 lo = e4m3x2_values(codes & 0xffffu), hi = e4m3x2_values(codes >> 16);
+      float f[4];
+      for (int x = 0; x < 4; ++x)
+        f[x] = __uint_as_float((uint32_t)min(max(row - col_byte[c0 + x] + 127, 0), 254) << 23);
+      w[r & 3][0] = e4m3x4(lo.x * f[0], lo.y * f[1], hi.x * f[2], hi.y * f[3]);
+    }
+    tile_put<16, 4>(tile, a, c0, w);
+  }
+}
+
 // One CTA per (block, 128 columns): codes transposed to q_t [cols, pitch] at column 128 blk, scales
 // to scale_t [., cols]. Rows past the expert's last are zeros. Tin uint8_t: E4M3 codes with 1 x 128
 // scale bytes in_scale [rows, ceil(cols / 128)] (an 8-bit checkpoint), read without a bf16 copy.
@@ -471,6 +516,8 @@ __global__ void __launch_bounds__(F8T_THREADS, sizeof(Tin) == 4 ? 2 : 4)
                                  uint8_t *__restrict__ q_t, size_t pitch,
                                  uint8_t *__restrict__ scale_t) {
   constexpr int V = 16 / sizeof(Tin), L = QB / V, A = F8T_THREADS / L, PASS = 32 / A;
+  constexpr bool CODES = sizeof(Tin) == 1;
+  __shared__ int loud;  // set by a value past fp32's largest (codes alone can stand for one)
   __shared__ __align__(16) uint32_t tile[QB * 32];
   __shared__ __align__(16) float cmax[F8T_THREADS / 32][QB];
   const KernelStamp stamp(K_F8B_QUANT);
@@ -522,6 +569,7 @@ __global__ void __launch_bounds__(F8T_THREADS, sizeof(Tin) == 4 ? 2 : 4)
     }
     if (lane < L) *(float4 *)&cmax[warp][c0 + 4 * j] = make_float4(m[0], m[1], m[2], m[3]);
   }
+  if (CODES && threadIdx.x == 0) loud = 0;
   __syncthreads();
   if (threadIdx.x < QB) {
     float x = 0.0f;
@@ -531,6 +579,7 @@ __global__ void __launch_bounds__(F8T_THREADS, sizeof(Tin) == 4 ? 2 : 4)
     if (ct * QB + (int)threadIdx.x < cols)
       scale_t[(size_t)blk * cols + ct * QB + threadIdx.x] = (uint8_t)b;
     cmax[0][threadIdx.x] = e8m0_inverse(b);
+    if (CODES && x > FLT_MAX) loud = 1;
   }
   __syncthreads();
 #pragma unroll
@@ -550,6 +599,13 @@ __global__ void __launch_bounds__(F8T_THREADS, sizeof(Tin) == 4 ? 2 : 4)
     tile_put<V>(tile, a0 + s * A, c0, w);
   }
   __syncthreads();
+  if (CODES && loud) {  // again, at the end, where the registers are free
+    find_token_block(offsets, E, rows, blk, &tb);
+    put_loud_tile((const uint8_t *)in + (size_t)tb.row0 * cols + ct * QB,
+                  in_scale + (size_t)tb.row0 * ntile + ct, cols, ntile, tb.n, cols - ct * QB, tile,
+                  (uint8_t *)cmax[1], scale_t + (size_t)blk * cols + ct * QB);
+    __syncthreads();
+  }
   tile_write<V>(tile, q_t + (size_t)ct * QB * pitch + (size_t)blk * QB, pitch, min(QB, cols - ct * QB),
                 QB);
   if (blockIdx.x == gridDim.x - 1 && threadIdx.x < 32) check_offsets(offsets, E, rows);
