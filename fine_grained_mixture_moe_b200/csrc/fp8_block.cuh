@@ -681,6 +681,13 @@ __global__ void __launch_bounds__(256, 4)
   }
 }
 
+// A block's scale in two factors: a code times the first is finite, the second (1 for the bytes up to 239)
+// is applied last. A gate of the larger bytes is 0 or past 2^104, and smaller by 2^9 it has the same
+// sigmoid and slope (1/2, 0 or 1).
+__device__ __forceinline__ float2 split_scale(uint32_t b) {
+  const bool big = b >= 240;
+  return make_float2(e8m0_value(big ? b - 9 : b), big ? 512.0f : 1.0f);
+}
 // From the checkpoint and dh: s = sigmoid(g), du = dh g s, dg = dh u s (1 + g (1 - s)), h = g s u.
 // dgu = [dg | du] in bf16 and / or as E4M3 codes (the input gradient's operand, quantised from the
 // fp32 values); h in bf16 (the down weight gradient's operand).
@@ -717,7 +724,7 @@ __global__ void __launch_bounds__(256, 4)
       sg = __ldg(gu_scale + at.off / QB);
       su = __ldg(gu_scale + at.off / QB + at.nb);
     }
-    const float vg = e8m0_value(sg), vu = e8m0_value(su);
+    const float2 vg = split_scale(sg), vu = split_scale(su);
     float dg[2][8], du[2][8];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -728,14 +735,14 @@ __global__ void __launch_bounds__(256, 4)
       for (int i = 0; i < 8; i += 2) {
         const float2 g2 = e4m3x2_values((wg[i / 4] >> (8 * (i % 4))) & 0xffffu);
         const float2 u2 = e4m3x2_values((wu[i / 4] >> (8 * (i % 4))) & 0xffffu);
-        const float gg[2] = {g2.x * vg, g2.y * vg}, uu[2] = {u2.x * vu, u2.y * vu};
+        const float gg[2] = {g2.x * vg.x, g2.y * vg.x}, uu[2] = {u2.x * vu.x, u2.y * vu.x};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float s = sigmoid_f(gg[j]), gs = gg[j] * s;
-          du[x][i + j] = d[i + j] * gs;
-          // s (1 + g (1 - s)) = s + g s (1 - s), at most 1.1: no overflow before the last factor
-          dg[x][i + j] = d[i + j] * fmaf(gs, 1.0f - s, s) * uu[j];
-          hv[i + j] = gs * uu[j];
+          du[x][i + j] = d[i + j] * gs * vg.y;
+          // s (1 + g (1 - s)) = s + g s (1 - s), at most 1.1: no overflow before the last factors
+          dg[x][i + j] = d[i + j] * fmaf(gs, 1.0f - s, s) * uu[j] * vu.y;
+          hv[i + j] = gs * uu[j] * (vg.y * vu.y);
         }
       }
       if (ok && dgu) {

@@ -2,6 +2,9 @@
 
 Tolerances, from the arithmetic alone:
 * token quantiser: exact, as every value code * 2^(byte - 127) has four significant bits.
+* SwiGLU backward: for |g| below 128 the bounds of the ordinary cases; from there on the sigmoid is
+  0 or 1 in fp32 (e^-128 < 2^-184), so an output errs by a few fp32 roundings (2^-22 of it); a
+  sigmoid below 2^-126 counts as 0.
 """
 import numpy as np
 import pytest
@@ -9,7 +12,7 @@ import torch
 
 from fine_grained_mixture_moe_b200 import binding as B
 from oracle import moe_fp8_block as FB
-from tests.test_gpu_fp8_block import DEV, check_device, np8, splits, u8
+from tests.test_gpu_fp8_block import DEV, check_codes, check_device, np8, splits, u8
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +92,93 @@ def test_quantize_tokens_of_the_largest_bf16_rows():
     rq, rs = FB.quantize_rows(x.float().cpu().numpy())
     assert np.array_equal(np8(q), rq) and np.array_equal(np8(s), rs) and rs.max() == 247
     check_tokens(rq, rs, np.array([0, 90, R], np.int32))
+
+
+# ------------------------------------------------------------------ SwiGLU backward
+def backward_errors(gu, dh):
+    """Reference (a sigmoid below 2^-126 counts as 0), and how far fp32 arithmetic may be off."""
+    f = dh.shape[1]
+    ref, rh = FB.swiglu_backward(gu, dh)
+    g, u, d = np.abs(gu[:, :f]), np.abs(gu[:, f:]), np.abs(dh)
+    s = 1.0 / (1.0 + np.exp(np.clip(-gu[:, :f], -700, 700)))
+    zero = s < 2.0 ** -126
+    ref, rh = np.where(np.tile(zero, 2), 0.0, ref), np.where(zero, 0.0, rh)
+    e1 = (8 + 1.2 * np.minimum(g, 128)) * 2.0 ** -23
+    near = g < 128
+    gn = np.where(near, g, 0.0)
+    e_slope = np.where(near, s * (1 + gn) * (e1 + 2.0 ** -22) + s * gn * (s * e1 + 2.0 ** -24), 0.0)
+    e_gs = np.where(near, gn * s * (e1 + 2.0 ** -22), 0.0)
+    border = np.where((s > 2.0 ** -127) & (s < 2.0 ** -125), s * (1 + g), 0.0)   # counts as 0 or not
+    e_dg = d * u * (e_slope + border) + 2.0 ** -22 * np.abs(ref[:, :f])
+    e_du = d * (e_gs + border) + 2.0 ** -22 * np.abs(ref[:, f:])
+    e_h = u * (e_gs + border) + 2.0 ** -22 * np.abs(rh)
+    # a first product below the normals of fp32 is kept to its last bit, 2^-149
+    gs, slope = g * s, s * (1 + gn * (1 - s))
+    e_dg += np.where(slope * u < 2.0 ** -126, d * 2.0 ** -149, 0.0)
+    e_du += np.where(gs < 2.0 ** -126, d * 2.0 ** -149, 0.0)
+    e_h += np.where(gs < 2.0 ** -126, u * 2.0 ** -149, 0.0)
+    return ref, np.concatenate([e_dg, e_du], 1) + 2.0 ** -148, rh, e_h + 2.0 ** -148
+
+
+def check_backward(gq, gs, dh, f, with_h):
+    R = gq.shape[0]
+    gu = FB.values_rows(gq, gs)
+    ref, err, rh, eh = backward_errors(gu, dh.astype(np.float64))
+    assert np.abs(ref).max() < 2.0 ** 127 and (not with_h or np.abs(rh).max() < 2.0 ** 127)
+    dgu = torch.full((R, 2 * f), -7.0, dtype=torch.bfloat16, device=DEV)
+    h = torch.full((R, f), -7.0, dtype=torch.bfloat16, device=DEV) if with_h else None
+    dq, ds = u8(R, 2 * f), u8(R, 2 * f // 128)
+    a = dev(gq, gs, dh)
+    B.moe_swiglu_fp8_backward(*a, R, f, dgu, dq, ds, h)
+    check_device()
+    # bf16 has fp32's exponents: half a step, or half the last bit of its subnormals
+    half = np.maximum(2.0 ** -8 * np.abs(ref), 2.0 ** -134)
+    assert np.all(np.abs(dgu.float().cpu().numpy() - ref) <= half + 2 * err)
+    if with_h:
+        assert np.all(np.abs(h.float().cpu().numpy() - rh) <= np.maximum(2.0 ** -8 * np.abs(rh), 2.0 ** -134) + 2 * eh)
+    check_codes(np8(dq), np8(ds), ref, err)
+
+
+@pytest.mark.parametrize("gate,up,dh_power,with_h", [
+    ((246, 254), (120, 130), -40, False),    # gates past the largest fp32 value
+    ((120, 124), (246, 254), -40, False),    # the other factor
+    ((246, 254), (246, 254), -60, False),
+    ((40, 70), (246, 254), -40, True),
+    ((246, 254), (60, 80), -60, True),
+    ((236, 244), (100, 110), -40, True),     # around the byte from which the scales are split
+    ((100, 110), (236, 244), -40, False),
+    ((1, 9), (1, 9), 0, True),
+    ((1, 9), (120, 130), 20, True),
+    ((30, 254), (60, 80), -20, True),
+])
+def test_swiglu_backward_of_any_scale_byte(gate, up, dh_power, with_h):
+    rng = np.random.default_rng(sum(gate) + 7 * sum(up))
+    R, f = 70, 256
+    gq = signed_codes(rng, (R, 2 * f))
+    gs = np.concatenate([rng.integers(gate[0], gate[1] + 1, (R, 2)),
+                         rng.integers(up[0], up[1] + 1, (R, 2))], 1).astype(np.uint8)
+    gs[0], gs[1] = [gate[0], gate[1], up[0], up[1]], [gate[1], gate[0], up[1], up[0]]
+    dh = (rng.uniform(1.0, 2.0, (R, f)) * 2.0 ** dh_power * rng.choice([-1, 1], (R, f))).astype(np.float32)
+    gq[2, :f] = 0
+    gq[3, f:] = 0x80
+    dh[4] = 0
+    check_backward(gq, gs, dh, f, with_h)
+
+
+def test_swiglu_of_the_largest_bf16_values_and_back():
+    """gate and up at the ends of bf16, through the forward's own checkpoint: no NaN, the formula's
+    derivative at the values that the checkpoint holds."""
+    R, f = 6, 128
+    big = torch.finfo(torch.bfloat16).max
+    gu = np.ones((R, 2 * f), np.float32)
+    gu[0, :f], gu[1, :f] = big, -big
+    gu[2, f:], gu[3, f:] = big, -big
+    gu[4, :f:2], gu[5, 1:f:2] = big, -big
+    t = torch.from_numpy(gu).to(torch.bfloat16).to(DEV)
+    gq, gs = u8(R, 2 * f), u8(R, 2 * f // 128)
+    B.moe_swiglu_fp8_forward(t, R, f, gu_q=gq, gu_scale=gs)
+    check_device()
+    rq, rs = FB.quantize_rows(gu)
+    assert np.array_equal(np8(gq), rq) and np.array_equal(np8(gs), rs)
+    dh = np.random.default_rng(4).uniform(-1e-3, 1e-3, (R, f)).astype(np.float32)
+    check_backward(rq, rs, dh, f, False)
