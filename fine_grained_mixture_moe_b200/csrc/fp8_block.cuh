@@ -740,8 +740,9 @@ __global__ void __launch_bounds__(256, 4)
         for (int j = 0; j < 2; ++j) {
           const float s = sigmoid_f(gg[j]), gs = gg[j] * s;
           du[x][i + j] = d[i + j] * gs * vg.y;
-          // s (1 + g (1 - s)) = s + g s (1 - s), at most 1.1: no overflow before the last factors
-          dg[x][i + j] = d[i + j] * fmaf(gs, 1.0f - s, s) * uu[j] * vu.y;
+          // s (1 + g (1 - s)) = s + g s (1 - s), between -0.1 and 1.1, times up's part (448 2^118 at most)
+          // first: dh times it could pass fp32's largest, or lose bits below its least normal number
+          dg[x][i + j] = fmaf(gs, 1.0f - s, s) * uu[j] * d[i + j] * vu.y;
           hv[i + j] = gs * uu[j] * (vg.y * vu.y);
         }
       }

@@ -142,6 +142,7 @@ def check_backward(gq, gs, dh, f, with_h):
 @pytest.mark.parametrize("gate,up,dh_power,with_h", [
     ((246, 254), (120, 130), -40, False),    # gates past the largest fp32 value
     ((120, 124), (246, 254), -40, False),    # the other factor
+    ((120, 128), (246, 254), -40, False),    # beside slopes down to 2^-126
     ((246, 254), (246, 254), -60, False),
     ((40, 70), (246, 254), -40, True),
     ((246, 254), (60, 80), -60, True),
@@ -163,6 +164,26 @@ def test_swiglu_backward_of_any_scale_byte(gate, up, dh_power, with_h):
     gq[3, f:] = 0x80
     dh[4] = 0
     check_backward(gq, gs, dh, f, with_h)
+
+
+def test_swiglu_backward_of_the_largest_gradient():
+    """A slope above 1 (at most 1.1, near g = 2.4) beside the largest dh, and an up that makes up for it."""
+    R, f = 2, 128
+    gu = np.full((R, 2 * f), 2.5, np.float32)
+    gu[:, f:] = [[2.0 ** -10], [-2.0 ** -3]]
+    gq, gs = FB.quantize_rows(gu)
+    dh = np.full((R, f), torch.finfo(torch.bfloat16).max / 8, np.float32)
+    dh[0] = 0.0
+    dh[1] *= 1.5
+    check_backward(gq, gs, dh, f, True)
+    # d_up alone leaves the range here, d_gate does not
+    dh = np.full((R, f), torch.finfo(torch.float32).max, np.float32)
+    dgu = torch.empty((R, 2 * f), dtype=torch.bfloat16, device=DEV)
+    B.moe_swiglu_fp8_backward(*dev(gq, gs, dh), R, f, dgu)
+    check_device()
+    ref, _ = FB.swiglu_backward(FB.values_rows(gq, gs), dh.astype(np.float64))
+    assert np.all(np.abs(dgu[:, :f].float().cpu().numpy() - ref[:, :f]) <=
+                  (2.0 ** -8 + 2.0 ** -20) * np.abs(ref[:, :f]))
 
 
 def test_swiglu_of_the_largest_bf16_values_and_back():
