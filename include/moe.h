@@ -399,7 +399,9 @@ moe_status_t moe_quantize_fp8_tokens(const void *in, int32_t in_dtype, const uin
  * a, a_scale: rows layout [rows, k]; w, w_scale: weight layout [E, n, k]; out [rows, n] in bf16 or
  * fp32 (out_dtype; 32-byte aligned), rounded once from fp32 sums. The input gradient is the same call on the
  * transposed weights. offsets may be NULL with E = 1: one weight for all rows. Rows outside every
- * expert are not written. */
+ * expert are not written. The tensor core adds 32 products at a time to a sum and cuts the result off
+ * to fp32 instead of rounding it: a sum over k errs by at most (k / 32 + 32) 2^-23 of the sum of its
+ * terms' magnitudes (terms of both signs average that out, terms of one sign do not). */
 moe_status_t moe_gemm_fp8_block(const uint8_t *a, const uint8_t *a_scale, int64_t rows,
                                 const int32_t *offsets, int32_t E, int32_t n, int32_t k,
                                 const uint8_t *w, const uint8_t *w_scale, void *out,
@@ -408,7 +410,9 @@ moe_status_t moe_gemm_fp8_block(const uint8_t *a, const uint8_t *a_scale, int64_
 /* Weight gradient: dw[e, c, i] = sum over the rows r of expert e of a[r, c] b[r, i], c < n, i < k
  * (a the product's upstream gradient, b its input), fp32 [E, n, k], 32-byte aligned; zeros for an
  * expert with no rows. a_t, a_scale: tokens layout of [rows, n]; b_t, b_scale: of [rows, k], both made with these
- * rows, offsets and E. */
+ * rows, offsets and E. The sum's error is the product's, with the expert's rows in k's place: at most
+ * 5e-4 of the sum of magnitudes for 131,072 rows (measured, terms of one sign: 5e-8 for 4,096 rows, 9e-5
+ * for 131,072, 2e-3 for 2^20; of both signs 4e-7 for 2^20). */
 moe_status_t moe_wgrad_fp8_block(const uint8_t *a_t, const uint8_t *a_scale, const uint8_t *b_t,
                                  const uint8_t *b_scale, int64_t rows, const int32_t *offsets,
                                  int32_t E, int32_t n, int32_t k, float *dw, void *stream);

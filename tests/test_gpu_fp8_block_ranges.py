@@ -1,10 +1,12 @@
-"""The block-scaled 8-bit operators at the ends of their ranges, against the fp64 oracle.
+"""The block-scaled 8-bit operators at the ends of their ranges, against the fp64 oracle: scale bytes
+from 1 to 254, the least codes, and sums and tile lists longer than the ordinary ones.
 
 Tolerances, from the arithmetic alone:
 * token quantiser: exact, as every value code * 2^(byte - 127) has four significant bits.
 * SwiGLU backward: for |g| below 128 the bounds of the ordinary cases; from there on the sigmoid is
   0 or 1 in fp32 (e^-128 < 2^-184), so an output errs by a few fp32 roundings (2^-22 of it); a
   sigmoid below 2^-126 counts as 0.
+* products: fp32 sums, see :func:`sum_tol`.
 """
 import numpy as np
 import pytest
@@ -12,7 +14,8 @@ import torch
 
 from fine_grained_mixture_moe_b200 import binding as B
 from oracle import moe_fp8_block as FB
-from tests.test_gpu_fp8_block import DEV, check_codes, check_device, np8, splits, u8
+from tests.test_gpu_fp8_block import (DEV, check_codes, check_device, np8, product_tol, row_blocks,
+                                      splits, u8)
 
 pytestmark = pytest.mark.gpu
 
@@ -203,3 +206,97 @@ def test_swiglu_of_the_largest_bf16_values_and_back():
     assert np.array_equal(np8(gq), rq) and np.array_equal(np8(gs), rs)
     dh = np.random.default_rng(4).uniform(-1e-3, 1e-3, (R, f)).astype(np.float32)
     check_backward(rq, rs, dh, f, False)
+
+
+# ------------------------------------------------------------------ products
+@pytest.mark.parametrize("R,n", [(3, 64), (16, 64), (600, 256)])
+@pytest.mark.parametrize("pair", [(1, 254), (254, 1), (1, 127), (10, 240), (240, 10), (14, 240), (1, 1)])
+@pytest.mark.parametrize("most", [0x07, 0x10, 0x38])
+def test_gemm_of_the_least_codes_at_both_ends(R, n, pair, most):
+    """Small codes under a small scale that a large one makes up for. A sum of products of codes is a
+    multiple of 2^-18 and the least scale 2^-126, so that even below fp32's normals, whose last bit
+    is 2^-149, applying the smaller scale first rounds nothing."""
+    rng = np.random.default_rng(R + sum(pair) + most)
+    k = 272
+    q, w = signed_codes(rng, (R, k), most), signed_codes(rng, (1, n, k), most)
+    q[:, ::5] = 0
+    s, ws = np.full((R, 3), pair[0], np.uint8), np.full((1, -(-n // 128), 3), pair[1], np.uint8)
+    out = torch.empty(R, n, device=DEV)
+    a, as_, b, bs = dev(q, s, w, ws)
+    B.moe_gemm_fp8_block(a, as_, R, None, 1, n, k, b, bs, out)
+    check_device()
+    offs = np.array([0, R])
+    A, W = FB.values_rows(q, s), FB.values_weight(w, ws)
+    ref, mag = FB.gemm(A, W, offs), FB.gemm(A, W, offs, absolute=True)
+    # an output below the normals is kept to fp32's last bit, in each of the sum's three blocks
+    tol = product_tol(ref, mag, k, "f32") + (3 * 2.0 ** -149 if sum(pair) < 127 else 0.0)
+    assert np.all(np.abs(out.cpu().numpy() - ref) <= tol)
+
+
+def sum_tol(ref, mag, K):
+    """A tile's sum stays in the tensor core's fp32 accumulator over all of K: one addition per 32 of K,
+    each off by at most one last bit (2^-23, a sum that is cut off, not rounded) of the sum of
+    magnitudes S, and 32 more for the additions within a step. The stored value is that fp32 sum."""
+    return (K / 32 + 32) * 2.0 ** -23 * mag
+
+
+def token_operand(vals, offs, nb):
+    """The tokens layout of `vals`, and the values its codes stand for, in row order."""
+    q, s = FB.quantize_tokens(vals, offs)
+    qf = np.full((vals.shape[1], 128 * nb), 0x7F, np.uint8)
+    sf = np.full((nb, vals.shape[1]), 250, np.uint8)
+    qf[:, :q.shape[1]], sf[:s.shape[0]] = q, s
+    v = FB.values_tokens(q, s).T
+    return qf, sf, np.concatenate([v[128 * b:128 * b + m] for b, m in row_blocks(offs)])
+
+
+@pytest.mark.parametrize("R,E,n,k", [(30000, 40, 640, 512), (30000, 40, 512, 640), (20000, 24, 1040, 448),
+                                     (60000, 300, 256, 240)])
+def test_wgrad_several_long_tiles_per_pair(R, E, n, k):
+    """More tiles than twice the CTA pairs, each of several blocks of K, an odd number of them among
+    them: the rounds' alternating direction, the ring of scale buffers and both accumulators over
+    long tiles, with either side as the rows, and with more experts than are put in order."""
+    rng = np.random.default_rng(R + E + n)
+    c = rng.multinomial(R, rng.dirichlet(np.full(E, 4.0)))
+    offs = np.concatenate([[0], np.cumsum(c)]).astype(np.int32)
+    nb = FB.token_blocks(R, E)
+    aq, as_, A = token_operand(rng.standard_normal((R, n)), offs, nb)
+    bq, bs, V = token_operand(rng.standard_normal((R, k)), offs, nb)
+    d = dev(aq, as_, bq, bs, offs)
+    dw = torch.full((E, n, k), -7.0, device=DEV)
+    B.moe_wgrad_fp8_block(*d[:4], R, d[4], E, n, k, dw)
+    check_device()
+    ref, mag = FB.wgrad(A, V, offs), FB.wgrad(A, V, offs, absolute=True)
+    longest = int(c.max())
+    assert np.all(np.abs(dw.cpu().numpy() - ref) <= sum_tol(ref, mag, longest))
+
+
+@pytest.mark.parametrize("R", [65536, 131072 + 40])
+def test_wgrad_of_one_sign(R):
+    """The longest sums, where nothing cancels: every product is positive."""
+    rng = np.random.default_rng(R)
+    n, k = 256, 48
+    offs = np.array([0, R], np.int32)
+    nb = FB.token_blocks(R, 1)
+    aq, as_, A = token_operand(np.abs(rng.standard_normal((R, n))) + 0.1, offs, nb)
+    bq, bs, V = token_operand(np.abs(rng.standard_normal((R, k))) + 0.1, offs, nb)
+    d = dev(aq, as_, bq, bs, offs)
+    dw = torch.full((1, n, k), -7.0, device=DEV)
+    B.moe_wgrad_fp8_block(*d[:4], R, d[4], 1, n, k, dw)
+    check_device()
+    ref = FB.wgrad(A, V, offs)
+    assert np.all(np.abs(dw.cpu().numpy() - ref) <= sum_tol(ref, ref, R))
+
+
+@pytest.mark.parametrize("R", [3, 600])
+def test_gemm_of_one_sign(R):
+    rng = np.random.default_rng(R)
+    n, k = 256, 65536 + 144
+    q, s = FB.quantize_rows(np.abs(rng.standard_normal((R, k))) + 0.1)
+    w, ws = FB.quantize_weight(np.abs(rng.standard_normal((1, n, k))) + 0.1)
+    out = torch.empty(R, n, device=DEV)
+    a, as_, b, bs = dev(q, s, w, ws)
+    B.moe_gemm_fp8_block(a, as_, R, None, 1, n, k, b, bs, out)
+    check_device()
+    ref = FB.gemm(FB.values_rows(q, s), FB.values_weight(w, ws), [0, R])
+    assert np.all(np.abs(out.cpu().numpy() - ref) <= sum_tol(ref, ref, k))
