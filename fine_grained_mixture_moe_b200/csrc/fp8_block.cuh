@@ -159,16 +159,10 @@ template <int V> __device__ __forceinline__ uint32_t amax_bits(const float (&v)[
   for (int i = 0; i < V; ++i) m = max(m, abs_bits(v[i]));
   return m;
 }
-// V codes of v * inv to q (V-byte aligned), V = 4, 8 or 16.
-template <int V> __device__ __forceinline__ void store_codes(uint8_t *q, const float (&v)[V], float inv) {
-  uint32_t w[V / 4];
-#pragma unroll
-  for (int i = 0; i < V / 4; ++i)
-    w[i] = e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
-  if (V == 4) *(uint32_t *)q = w[0];
-  if (V == 8) *(uint2 *)q = make_uint2(w[0], w[V / 4 > 1 ? 1 : 0]);
-  if (V == 16)
-    *(uint4 *)q = make_uint4(w[0], w[V / 4 > 1 ? 1 : 0], w[V / 4 > 2 ? 2 : 0], w[V / 4 > 3 ? 3 : 0]);
+// 8 codes of v * inv to q (8-byte aligned).
+__device__ __forceinline__ void store_codes(uint8_t *q, const float (&v)[8], float inv) {
+  *(uint2 *)q = make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                           e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
 }
 __device__ __forceinline__ void store_bf16x8(__nv_bfloat16 *p, const float (&v)[8]) {
   uint32_t w[4];

@@ -23,6 +23,7 @@
 #define MOE_F8B_TILES ((1ll << 31) - 65536)
 
 static inline bool f8b_dtype(int32_t t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32; }
+// a product's output: its rows, multiples of 32 bytes, then fill whole sectors of L2
 static inline bool aligned32(const void *p) { return p && ((uintptr_t)p & 31u) == 0; }
 static inline bool aligned4(const void *p) { return p && ((uintptr_t)p & 3u) == 0; }
 
