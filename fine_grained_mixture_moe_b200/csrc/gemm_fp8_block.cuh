@@ -49,6 +49,9 @@ constexpr int F8G_STG = F8G_STORE_WARPS * 4096;  // staging of 32 rows x 128 byt
 constexpr int F8G_SF_BUFS = 4;       // scale buffers ...
 constexpr int F8G_SF_K = 4;          // ... of four K blocks
 constexpr int F8G_SF_BYTES = 2 * 384 * 4;  // their words on the way to TMEM
+// The wait for a finished tile lasts as long as the tile, without a bound on K (a weight gradient of 2^31
+// rows has 2^24 blocks): its limit grows by four times what a block takes at the power cap's clocks.
+constexpr uint64_t F8G_BLOCK_NS = 2000;
 
 struct F8Gemm {
   CUtensorMap ma, mb;
@@ -514,7 +517,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8G_THREADS, 1)
       const int rbase = t.m0 + (int)rank * 128 + q * 32;
       const int nrows = min(32, t.rows - rbase), ncols = min(p.tn, p.N - t.n0);
       if (t.nk > 0) {
-        if (!f8_wait_warp(accf_bar(acc), acc_phase, abort_flag, limit, INFO_WAIT_ACC_FULL)) break;
+        if (!f8_wait_warp(accf_bar(acc), acc_phase, abort_flag, limit + F8G_BLOCK_NS * t.nk, INFO_WAIT_ACC_FULL))
+          break;
         tc_fence_after();
       }
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);

@@ -300,3 +300,28 @@ def test_gemm_of_one_sign(R):
     check_device()
     ref = FB.gemm(FB.values_rows(q, s), FB.values_weight(w, ws), [0, R])
     assert np.all(np.abs(out.cpu().numpy() - ref) <= sum_tol(ref, ref, k))
+
+
+def test_wgrad_tile_longer_than_a_wait():
+    """One tile whose sum takes longer than the bound on a single wait: each step comes in time, so no wait
+    may run out, the one for the finished tile among them."""
+    R, n = 1 << 22, 16
+    offs = torch.tensor([0, R], dtype=torch.int32, device=DEV)
+    nb = B.moe_fp8_token_blocks(R, 1)
+    x = torch.randn((R, n), device=DEV).to(torch.bfloat16)
+    q, s = u8(n, 128 * nb), u8(nb, n)
+    B.moe_quantize_fp8_tokens(x, None, R, n, offs, 1, q, s)
+    outs = [torch.full((1, n, n), -7.0, device=DEV) for _ in range(2)]
+    B.moe_wgrad_fp8_block(q, s, q, s, R, offs, 1, n, n, outs[0])
+    check_device()
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    B.moe_debug_set(B.DEBUG_WAIT_LIMIT_NS, 1_000_000)
+    try:
+        start.record()
+        B.moe_wgrad_fp8_block(q, s, q, s, R, offs, 1, n, n, outs[1])
+        end.record()
+        check_device()
+    finally:
+        B.moe_debug_set(B.DEBUG_WAIT_LIMIT_NS, 2_000_000_000)
+    assert start.elapsed_time(end) > 1.0                     # (the case is what it says)
+    assert torch.equal(outs[0], outs[1])
