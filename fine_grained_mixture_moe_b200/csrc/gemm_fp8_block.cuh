@@ -8,15 +8,16 @@
 //   128 start[g] .. 128 start[g + 1] of a_t [n, pitch] and b_t [k, pitch],
 //   dw[g][r, c] = sum over its blocks tb of 2^(sa[tb, r] + sb[tb, c]) sum over t in tb of a_t b_t.
 //
-// The scales are applied by the tensor core (kind::mxf8f6f4, block_scale): one E8M0 byte per row of
-// A and per row of B for each K = 32 instruction, read from TMEM. A TMEM word holds four bytes and the
-// instruction names one of them, so a word serves four blocks of 128, and the four instructions of a
-// block name the same byte. The fp32 accumulator of a tile stays in TMEM over the whole of K and is
-// read once; each instruction's addition to it is cut off, not rounded, so that sums of one sign lose up
-// to 2^-23 of themselves per 32 of K (3e-5 measured at K = 65,536). Steps of the Quartz gate|up product (24,576 rows, n 1,280, k 1,024, six experts): scales
-// applied outside, a TMEM read and an fp32 multiply-add of every element per block of K, 59.6 us; in the
-// tensor core, one block per scale word, 42.0; four blocks per word, read once per CTA, 36.0; streaming
-// stores and the issuing thread's loop unrolled over a stage, 35.0.
+// The scales are applied by the tensor core (kind::mxf8f6f4, block_scale): one E8M0 byte per row of A and
+// per row of B for each K = 32 instruction, read from TMEM. A TMEM word holds four bytes and the
+// instruction names one of them, so a word serves four blocks of 128, and the four instructions of a block
+// name the same byte. The fp32 accumulator of a tile stays in TMEM over the whole of K and is read once;
+// each instruction's addition to it is cut off, not rounded, so that sums of one sign lose up to 2^-23 of
+// themselves per 32 of K (3e-5 measured at K = 65,536). Steps of the Quartz gate|up product (24,576 rows,
+// n 1,280, k 1,024, six experts): scales applied outside, a TMEM read and an fp32 multiply-add of every
+// element per block of K, 59.6 us; in the tensor core, one block per scale word, 42.0; four blocks per
+// word, read once per CTA, 36.0; streaming stores and the issuing thread's loop unrolled over a stage,
+// 35.0.
 //
 // Clusters, stages and barriers are those of gemm_tc2.cuh: a tile of 256 x N (N = 16 .. 224) per CTA
 // pair, CTA r loads rows 128 r .. of the A tile and half of the N rows of B, the leader issues
@@ -28,14 +29,18 @@
 // rows per column, one per lane).
 //
 // Bound: the operands' way from L2. A stage is 60 KB per CTA for about 950 cycles of the tensor core;
-// three stages (all that shared memory holds) cycle in about 1,310, i.e. 46 bytes per cycle and SM
-// (13 TB/s in all), and the tensor pipe is 72% busy between tiles, 40% over the Quartz call (35.0 - 35.4
-// us, 1.8 PFLOP/s, start-up and last stores included), 2.3 PFLOP/s at 131,072 x 1,536 x 1,536 (265 -
-// 273 us; 316 - 325 at the clocks of the power cap, 1,300 MHz, when repeated for seconds). One block per stage (43 us), wider spacing of the tiles' K order (53 us: concurrent reads of
-// one line no longer meet), narrower tiles (47.5 us at 192), L2 prefetches and stores by the TMA unit
-// (37 us each) were slower. The weight gradient's fp32 output is its second bound: 52 us for the Quartz
-// gate|up gradient on six experts (32 blocks of K each, the rest zeros; 60 with the other side as
-// rows, 25 tiles per expert instead of 24), 50 us with the rows spread over all 24 (56 in expert order).
+// three stages (all that shared memory holds) cycle in about 1,350, i.e. 45 bytes per cycle and SM (13
+// TB/s in all), and a tile of four stages takes 6,000, 63% of them the tensor core's. Over the Quartz call
+// with its rows on all 24 experts the pipe is 46% busy (39.5 us, 1.6 PFLOP/s, start-up and last stores
+// included; 35.0 us on six experts). 131,072 x 1,536 x 1,536: 280 us on 48 experts, 268 on four (2.2 - 2.3
+// PFLOP/s; 316 - 326 at the clocks of the power cap, 1,300 MHz, when repeated for seconds). One block per
+// stage (43 us against 36), wider spacing of the tiles' K order (53 us: concurrent reads of one line no
+// longer meet), narrower tiles (47.5 us at 192), L2 prefetches and stores by the TMA unit (37 us each)
+// were slower. The weight gradient waits for its operands too (a tile is stored before its accumulator is
+// needed again), beside 126 MB of fp32 stores: the Quartz gate|up gradient takes 49 - 54 us with the rows
+// on all 24 experts (56 in expert order). On six of them (32 blocks of K each, the rest zeros) the same
+// binary took 52 to 80 us in different processes, 61 and 72 on one machine, for a reason not found; the
+// side that gives 24 tiles per expert instead of 25 as rows took 52 against 60.
 #pragma once
 #include "fp8_block.cuh"
 #include "gemm_tc2.cuh"

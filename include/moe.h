@@ -355,7 +355,8 @@ moe_status_t moe_quantize_fp8(const void *in, int32_t in_dtype, int64_t rows, in
  *           through the experts in order; q_t [cols, 128 * B], scale_t [B, cols], with
  *           B = moe_fp8_token_blocks(rows, E), which holds any split of `rows` rows. Rows that
  *           complete an expert's last block are zeros; blocks past the last are not written.
- * A last block along a dimension may be shorter. Scale bytes 1 .. 254 are valid on input.
+ * A last block along a dimension may be shorter. Scale bytes 1 .. 254 are valid on input; the values that
+ * codes stand for may pass fp32's largest as long as an operator's outputs do not.
  *
  * For all of them: widths (cols, n, k; rows of a weight) are multiples of 16 up to 2^20,
  * 1 <= E <= 1024, rows < 2^31 - 4096 (more returns MOE_ERR_UNSUPPORTED), rows = 0 writes nothing
